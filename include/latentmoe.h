@@ -439,6 +439,94 @@ int latentmoe_last_cuda_error(latentmoe_t h);
 /* Static description of a return code. */
 const char* latentmoe_strerror(int code);
 
+/* ---- Orthogonalised matrix updates (Muon with Newton-Schulz products). ---
+ * "Frontier Pre-training at Microsoft AI" and "MAI-Base-2: Microsoft's 2.8T
+ * base model, and whether its compute numbers add up" name Muon with
+ * Newton-Schulz iterations as these layers' optimiser. For each matrix of a
+ * stack [batch, rows, cols] (an expert stack such as w_g [E, F, l] is one):
+ *
+ *   X_0 = U / (|U|_F + eps)
+ *   X  <- a X + (b A + c A^2) X,  A = X X^T       (rows <= cols)
+ *   X  <- a X + X (b A + c A^2),  A = X^T X       (rows >  cols)
+ *
+ * for every (a, b, c) of the coefficients: the singular values of U move to
+ * the neighbourhood of 1, its singular vectors stay. Products of fp16
+ * operands with power-of-two scales and fp32 accumulation; X, the norms and
+ * the momentum are fp32. The result is within about 2e-3 of its norm of the
+ * exact iteration's, its rounding to bf16 included. A matrix of zeros gives
+ * zeros; a NaN or an infinity makes its own matrix NaN, not the others. The
+ * squared norm is held in fp32 (norms below 1.8e19). Results are bitwise
+ * reproducible. */
+typedef struct latentmoe_muon* latentmoe_muon_t;
+
+enum { LATENTMOE_BF16 = 0, LATENTMOE_FP32 = 1 }; /* element types of g and w below */
+
+/* batch 1..65535, rows and cols 1..65536 (any size: no multiples needed),
+ * steps 1..32. coefs: host [steps][3] = (a, b, c) of each step, or NULL for
+ * (3.4445, -4.7750, 2.0315) in every step. eps >= 1e-30. */
+typedef struct {
+  int64_t batch;
+  int64_t rows;
+  int64_t cols;
+  int64_t steps;
+  const float* coefs;
+  float eps;
+} latentmoe_muon_dims;
+
+/* One optimiser step, all tensors contiguous device [batch, rows, cols]:
+ *   m <- momentum_coef m + g;  U = g + momentum_coef m (nesterov) or m
+ *   w <- (1 - lr weight_decay) w - lr scale X
+ * g bf16 or fp32, momentum fp32, w bf16 or fp32 (g_dtype, w_dtype). */
+typedef struct {
+  const void* g;
+  float* momentum;
+  void* w;
+  int32_t g_dtype;
+  int32_t w_dtype;
+  int32_t nesterov;
+  float lr;
+  float momentum_coef;
+  float weight_decay;
+  float scale;
+} latentmoe_muon_update;
+
+/* Create a handle on the current device; allocates the workspace (X in fp32
+ * and twice in fp16, two fp16 matrices of min(rows, cols)^2: per matrix 8
+ * rows cols + 4 min(rows, cols)^2 bytes). The handle follows the rules of a
+ * layer handle: one host thread and one stream at a time, one device.
+ * Errors: INVALID_ARG (NULL, a size or steps < 1, eps out of range,
+ * coefficients that are not finite or under which a singular value in [0, 1]
+ * grows beyond 1e6), UNSUPPORTED (beyond the limits above), OUT_OF_MEMORY,
+ * CUDA. On error *out is NULL and nothing stays allocated. */
+int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out);
+
+/* out (bf16) = the iteration's X for U = g; g of type g_dtype; both
+ * contiguous device [batch, rows, cols]. out may be g itself if g is bf16,
+ * and may not overlap it otherwise. Asynchronous on `stream`, 2 + 3 steps
+ * launches, no host synchronisation: it can be captured into a CUDA graph
+ * once a first call outside the capture has set up the kernels. Errors:
+ * INVALID_ARG (NULL, unknown type), UNSUPPORTED (pointer not 16-byte
+ * aligned), CUDA. */
+int latentmoe_muon_orthogonalize(latentmoe_muon_t h, const void* g, int g_dtype, void* out,
+                                 latentmoe_stream_t stream);
+
+/* The optimiser step above; momentum and w are updated in place and must not
+ * overlap each other or g. Otherwise as latentmoe_muon_orthogonalize; also
+ * INVALID_ARG when lr, momentum_coef, weight_decay or scale is not finite. */
+int latentmoe_muon_step(latentmoe_muon_t h, const latentmoe_muon_update* u,
+                        latentmoe_stream_t stream);
+
+/* Tiles of the products: 0 = 128 x 128 on single SMs, 1 = 256 x 256 on SM
+ * pairs, 2 (the default) = whichever takes fewer rounds of tiles. */
+int latentmoe_muon_set_sm_pairs(latentmoe_muon_t h, int mode);
+
+/* As latentmoe_get_status, latentmoe_get_launch_count, latentmoe_last_cuda_error
+ * and latentmoe_destroy, for a Muon handle. */
+int latentmoe_muon_get_status(latentmoe_muon_t h, uint32_t* device_status);
+int latentmoe_muon_get_launch_count(latentmoe_muon_t h, int64_t* launches);
+int latentmoe_muon_last_cuda_error(latentmoe_muon_t h);
+int latentmoe_muon_destroy(latentmoe_muon_t h);
+
 /* ---- Debug entry points: the tensor-core GEMM core on its own. ----------
  * C = epilogue(A B^T) for bf16 A [M, K] and B [N', K] (device, row-major).
  *   mode 0: C bf16 [M, N], B has N rows

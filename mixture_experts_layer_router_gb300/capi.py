@@ -33,6 +33,9 @@ FP8_EXPERTS = 16
 FP8_DENSE = 32
 FP8_TENSORS = 5  # scaled activations: z, h, x, c, shared hidden
 
+BF16 = 0  # element types of a matrix update
+FP32 = 1
+
 STATUS_TIMEOUT = 1
 STATUS_BAD_EXPERT = 2
 STATUS_ROUNDS = 4
@@ -50,6 +53,19 @@ class latentmoe_dims(ctypes.Structure):
 class latentmoe_weights(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in
                 ("w_r", "b_r", "w_dn", "w_g", "w_u", "w_d", "w_up", "w_gs", "w_us", "w_ds")]
+
+
+class latentmoe_muon_dims(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("rows", _i64), ("cols", _i64), ("steps", _i64),
+                ("coefs", ctypes.POINTER(ctypes.c_float)), ("eps", ctypes.c_float)]
+
+
+class latentmoe_muon_update(ctypes.Structure):
+    _fields_ = [("g", _c_void_p), ("momentum", _c_void_p), ("w", _c_void_p),
+                ("g_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32), ("lr", ctypes.c_float),
+                ("momentum_coef", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float)]
 
 
 # name -> (restype, argtypes)
@@ -102,6 +118,17 @@ SIGNATURES = {
                                                _c_void_p, _c_void_p]),
     "latentmoe_debug_grouped_gemm_e4m3": (ctypes.c_int, [_c_void_p] * 6 + [_i64] * 4 +
                                           [ctypes.c_int, _c_void_p]),
+    "latentmoe_muon_create": (ctypes.c_int, [ctypes.POINTER(latentmoe_muon_dims),
+                                             ctypes.POINTER(_c_void_p)]),
+    "latentmoe_muon_orthogonalize": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _c_void_p,
+                                                    _c_void_p]),
+    "latentmoe_muon_step": (ctypes.c_int, [_c_void_p, ctypes.POINTER(latentmoe_muon_update),
+                                           _c_void_p]),
+    "latentmoe_muon_set_sm_pairs": (ctypes.c_int, [_c_void_p, ctypes.c_int]),
+    "latentmoe_muon_get_status": (ctypes.c_int, [_c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
+    "latentmoe_muon_get_launch_count": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
+    "latentmoe_muon_last_cuda_error": (ctypes.c_int, [_c_void_p]),
+    "latentmoe_muon_destroy": (ctypes.c_int, [_c_void_p]),
     "latentmoe_debug_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "latentmoe_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64,
                                                     ctypes.POINTER(ctypes.c_uint32)]),
@@ -376,6 +403,108 @@ class LatentMoE:
         v = _i64(0)
         check(load().latentmoe_get_launch_count(self.handle, ctypes.byref(v)),
               "latentmoe_get_launch_count")
+        return v.value
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype_code(t, name: str) -> int:
+    import torch
+    _need(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bfloat16 or float32")
+    return FP32 if t.dtype == torch.float32 else BF16
+
+
+class Muon:
+    """A handle that orthogonalises updates of a stack of ``batch`` matrices
+    [rows, cols] by Newton-Schulz products. ``coefs``: one (a, b, c) for every
+    step, or a list of ``steps`` of them; None for the library's default."""
+
+    def __init__(self, rows: int, cols: int, batch: int = 1, steps: int = 5, coefs=None,
+                 eps: float = 1e-7):
+        lib = load()
+        arr = None
+        if coefs is not None:
+            flat = [float(v) for c in coefs for v in (c if hasattr(c, "__len__") else (c,))]
+            if len(flat) == 3:
+                flat = flat * steps
+            _need(len(flat) == 3 * steps, "coefs must be (a, b, c) or one (a, b, c) per step")
+            arr = (ctypes.c_float * len(flat))(*flat)
+        self.dims = latentmoe_muon_dims(batch, rows, cols, steps,
+                                        ctypes.cast(arr, ctypes.POINTER(ctypes.c_float))
+                                        if arr is not None else None, eps)
+        h = _c_void_p()
+        check(lib.latentmoe_muon_create(ctypes.byref(self.dims), ctypes.byref(h)),
+              "latentmoe_muon_create")
+        self.dims.coefs = None  # the library has copied them
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            load().latentmoe_muon_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check(self, code: int, what: str) -> None:
+        if code != OK:
+            raise LatentMoEError(code, what, load().latentmoe_muon_last_cuda_error(self.handle))
+
+    def _matrices(self, t, name: str) -> None:
+        d = self.dims
+        _need(t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous CUDA tensor")
+        shape = tuple(t.shape) if t.dim() == 3 else (1,) + tuple(t.shape)
+        _need(shape == (d.batch, d.rows, d.cols),
+              f"{name} must be [{d.batch}, {d.rows}, {d.cols}], got {list(t.shape)}")
+
+    def orthogonalize(self, g, out=None, stream=None):
+        """The orthogonalised g (bf16 or fp32), in bf16."""
+        import torch
+        self._matrices(g, "g")
+        if out is None:
+            out = torch.empty_like(g, dtype=torch.bfloat16)
+        else:
+            self._matrices(out, "out")
+            _need(out.dtype == torch.bfloat16, "out must be bfloat16")
+        self._check(load().latentmoe_muon_orthogonalize(
+            self.handle, g.data_ptr(), _dtype_code(g, "g"), out.data_ptr(), _stream(stream)),
+            "latentmoe_muon_orthogonalize")
+        return out
+
+    def step(self, w, g, momentum, lr: float, momentum_coef: float = 0.95,
+             weight_decay: float = 0.0, scale: float = 1.0, nesterov: bool = True,
+             stream=None) -> None:
+        """One optimiser step: momentum (fp32) and w (bf16 or fp32) in place."""
+        import torch
+        for t, name in ((w, "w"), (g, "g"), (momentum, "momentum")):
+            self._matrices(t, name)
+        _need(momentum.dtype == torch.float32, "momentum must be float32")
+        u = latentmoe_muon_update(g.data_ptr(), momentum.data_ptr(), w.data_ptr(),
+                                  _dtype_code(g, "g"), _dtype_code(w, "w"), int(nesterov), lr,
+                                  momentum_coef, weight_decay, scale)
+        self._check(load().latentmoe_muon_step(self.handle, ctypes.byref(u), _stream(stream)),
+                    "latentmoe_muon_step")
+
+    def set_sm_pairs(self, mode: int) -> None:
+        """0: 128 x 128 tiles on single SMs; 1: 256 x 256 on SM pairs; 2: automatic."""
+        self._check(load().latentmoe_muon_set_sm_pairs(self.handle, int(mode)),
+                    "latentmoe_muon_set_sm_pairs")
+
+    def status(self) -> int:
+        v = ctypes.c_uint32(0)
+        load().latentmoe_muon_get_status(self.handle, ctypes.byref(v))
+        return v.value
+
+    def launch_count(self) -> int:
+        v = _i64(0)
+        self._check(load().latentmoe_muon_get_launch_count(self.handle, ctypes.byref(v)),
+                    "latentmoe_muon_get_launch_count")
         return v.value
 
 

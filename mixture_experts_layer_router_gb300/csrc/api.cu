@@ -39,6 +39,7 @@
 #include "gemm_fused.cuh"
 #include "kernels.h"
 #include "latentmoe.h"
+#include "tensor_map.h"
 
 using lmoe::GemmArgs;
 using lmoe::GemmMaps;
@@ -54,23 +55,9 @@ const char* const kStageNames[kNumStages] = {
 constexpr int kFp8Acts = LATENTMOE_FP8_TENSORS;
 constexpr int kDenseW = 5;  // E4M3 dense weights: W_dn, W_up, W_gs, W_us, W_ds
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using lmoe::EncodeTiledFn;
 
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
+EncodeTiledFn encode_fn() { return lmoe::tensor_map_encoder(); }
 
 // 2-D bf16 tensor [rows, cols] (row stride `ld` elements) read in boxes of
 // 64 columns x box_rows rows with 128-byte swizzle; out-of-range reads are 0.

@@ -1,0 +1,39 @@
+// Launchers of the Newton-Schulz kernels (internal interface).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ns_gemm.cuh"
+
+namespace lmoe {
+
+// Update U of each matrix from gradient and momentum, and the partial sums of
+// its squares: partial[b * chunks + c] over chunk c of matrix b (n elements a
+// matrix). momentum null: U = G. One launch.
+constexpr int kNsMaxChunks = 1024;
+constexpr int kNsNormThreads = 256;
+struct NsUpdate {
+  const void* g;
+  bool g_f32;
+  float* momentum;  // [batch, n] or null
+  float mu;
+  bool nesterov;
+};
+cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int chunks,
+                           long long chunk, float* partial, cudaStream_t s);
+
+// X_0 = U / (|U|_F + eps): x32 [batch, rows, ld] and its fp16 copy times
+// `scale`; the padding columns are zero. U is formed as by launch_ns_norm from
+// the momentum that launch updated.
+cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, long long cols,
+                           long long ld, int chunks, const float* partial, float eps, float scale,
+                           float* x32, __half* x16, cudaStream_t s);
+
+// One product. epi: NsEpi; tall: X has more rows than columns; pair: tiles of
+// 256 x 256 on SM pairs instead of 128 x 128 on single SMs. ma, mb: 3-D maps
+// (boxes of 64 columns x 64 rows x 1) of the two operands.
+cudaError_t launch_ns_gemm(int epi, bool tall, bool pair, const CUtensorMap& ma,
+                           const CUtensorMap& mb, const NsArgs& a, int sms, cudaStream_t s);
+
+}  // namespace lmoe
