@@ -298,6 +298,66 @@ int latentmoe_route_from_logits_static(const float* logits, int64_t T, int64_t E
 int latentmoe_lbl_stats(latentmoe_t h, float* prob_sum, int32_t* counts,
                         latentmoe_stream_t stream);
 
+/* The router's balance loss and what its gradient needs. The pages name a
+ * load-balancing loss (sections as for latentmoe_lbl_stats) without a
+ * formula; this is the product of load and mean probability, with an optional
+ * penalty on the log-sum-exp. T tokens form S = T / seq_len sequences
+ * (seq_len 0: one of T tokens, the loss over the whole batch). A token counts
+ * if valid[t] != 0 (valid NULL: all) and its logits are not all -inf; N_s
+ * tokens of sequence s count. With p the softmax of a token's logits:
+ *   counts[s,e]   = slots (t, j) of counting tokens with idx[t,j] = e
+ *   prob_sum[s,e] = sum of p[t,e],  z_sum[s] = sum of lse_t^2,
+ *   lse_t = log sum_e exp(logits[t,e]),  tokens[s] = N_s
+ *   balance = 1/S sum_s E/(k N_s^2) sum_e counts[s,e] prob_sum[s,e]
+ *   z       = 1/S sum_s z_sum[s] / N_s          (terms with N_s = 0 are 0)
+ *   loss    = {balance_coef balance + z_coef z, balance, z}
+ * Every array is fp32 or int32 on the device. NaN logits of a counting token
+ * make the loss NaN. Expert ids outside [0, E) are not counted and set
+ * LATENTMOE_STATUS_BAD_EXPERT. */
+typedef struct {
+  int32_t* counts;  /* [S, E] */
+  float* prob_sum;  /* [S, E] */
+  float* z_sum;     /* [S] */
+  int32_t* tokens;  /* [S] */
+} latentmoe_balance_stats;
+
+/* Forward, one launch on `stream`: stats and loss [3] from fp32 logits [T, E]
+ * with row stride ld (0: E), idx [T, k] int32 and valid [T] bytes or NULL.
+ * 1 <= T <= max_tokens, seq_len divides T; E and k are the handle's. No
+ * weights need to be loaded. Bitwise deterministic. The sums of several
+ * micro-batches or ranks may be added and passed to the other two entries.
+ * Errors: INVALID_ARG (NULL but for valid, sizes, ld < E, coefficients not
+ * finite), UNSUPPORTED (logits not 16-byte aligned), CUDA. */
+int latentmoe_balance_loss(latentmoe_t h, const float* logits, int64_t ld, const int32_t* idx,
+                           const uint8_t* valid, int64_t T, int64_t seq_len,
+                           float balance_coef, float z_coef,
+                           const latentmoe_balance_stats* stats, float* loss,
+                           latentmoe_stream_t stream);
+
+/* loss [3] from the stats of `sequences` sequences (1..max_tokens), such as
+ * sums over ranks: the global-batch loss. */
+int latentmoe_balance_loss_from_stats(latentmoe_t h, const latentmoe_balance_stats* stats,
+                                      int64_t sequences, float balance_coef, float z_coef,
+                                      float* loss, latentmoe_stream_t stream);
+
+/* The gradient with respect to the logits of d_loss * loss[0] (d_loss: device
+ * fp32 [1], NULL: 1) plus sum d_gates * gates, the gates being the handle's
+ * (softmax probabilities of idx, divided by their sum with LATENTMOE_RENORM);
+ * d_gates fp32 [T, k] or NULL for the loss alone (idx may then be NULL too).
+ * counts [S, E] and tokens [S] are the forward's, or sums over ranks and
+ * micro-batches (the counts carry no gradient). The loss's part is zero for
+ * tokens that do not count; the gates' part is given for every token. Ids
+ * outside [0, E) contribute nothing; repeated ids of a token add up. d_logits
+ * [T, E] fp32 with row stride ldd (0: E) is written whole, and may be logits
+ * itself where ldd = ld. One launch; asynchronous; deterministic. Errors as
+ * latentmoe_balance_loss. */
+int latentmoe_router_backward(latentmoe_t h, const float* logits, int64_t ld,
+                              const int32_t* idx, const float* d_gates, const uint8_t* valid,
+                              const int32_t* counts, const int32_t* tokens, int64_t T,
+                              int64_t seq_len, float balance_coef, float z_coef,
+                              const float* d_loss, float* d_logits, int64_t ldd,
+                              latentmoe_stream_t stream);
+
 /* Copy the routing state of the last forward on this handle into caller
  * device buffers (each may be NULL): logits [T, E] fp32 (bias included),
  * idx, gates, counts, offsets, perm, pos as in latentmoe_route_from_logits.
@@ -490,9 +550,8 @@ typedef struct {
   float scale;
 } latentmoe_muon_update;
 
-/* Create a handle on the current device; allocates the workspace (X in fp32
- * and twice in fp16, two fp16 matrices of min(rows, cols)^2: per matrix 8
- * rows cols + 4 min(rows, cols)^2 bytes). The handle follows the rules of a
+/* Create a handle on the current device; allocates the workspace (per matrix
+ * about 8 rows cols + 4 min(rows, cols)^2 bytes). The handle follows the rules of a
  * layer handle: one host thread and one stream at a time, one device.
  * Errors: INVALID_ARG (NULL, a size or steps < 1, eps out of range,
  * coefficients that are not finite or under which a singular value in [0, 1]
@@ -502,9 +561,9 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
 
 /* out (bf16) = the iteration's X for U = g; g of type g_dtype; both
  * contiguous device [batch, rows, cols]. out may be g itself if g is bf16,
- * and may not overlap it otherwise. Asynchronous on `stream`, 2 + 3 steps
- * launches, no host synchronisation: it can be captured into a CUDA graph
- * once a first call outside the capture has set up the kernels. Errors:
+ * and may not overlap it otherwise. Asynchronous on `stream`, 3 launches, no
+ * host synchronisation: it can be captured into a CUDA graph once a first
+ * call outside the capture has set up the kernels. Errors:
  * INVALID_ARG (NULL, unknown type), UNSUPPORTED (pointer not 16-byte
  * aligned), CUDA. */
 int latentmoe_muon_orthogonalize(latentmoe_muon_t h, const void* g, int g_dtype, void* out,

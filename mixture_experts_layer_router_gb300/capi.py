@@ -55,6 +55,10 @@ class latentmoe_weights(ctypes.Structure):
                 ("w_r", "b_r", "w_dn", "w_g", "w_u", "w_d", "w_up", "w_gs", "w_us", "w_ds")]
 
 
+class latentmoe_balance_stats(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in ("counts", "prob_sum", "z_sum", "tokens")]
+
+
 class latentmoe_muon_dims(ctypes.Structure):
     _fields_ = [("batch", _i64), ("rows", _i64), ("cols", _i64), ("steps", _i64),
                 ("coefs", ctypes.POINTER(ctypes.c_float)), ("eps", ctypes.c_float)]
@@ -118,6 +122,17 @@ SIGNATURES = {
                                                _c_void_p, _c_void_p]),
     "latentmoe_debug_grouped_gemm_e4m3": (ctypes.c_int, [_c_void_p] * 6 + [_i64] * 4 +
                                           [ctypes.c_int, _c_void_p]),
+    "latentmoe_balance_loss": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                              _i64, _i64, ctypes.c_float, ctypes.c_float,
+                                              ctypes.POINTER(latentmoe_balance_stats), _c_void_p,
+                                              _c_void_p]),
+    "latentmoe_balance_loss_from_stats": (ctypes.c_int,
+                                          [_c_void_p, ctypes.POINTER(latentmoe_balance_stats),
+                                           _i64, ctypes.c_float, ctypes.c_float, _c_void_p,
+                                           _c_void_p]),
+    "latentmoe_router_backward": (ctypes.c_int, [_c_void_p, _c_void_p, _i64] + [_c_void_p] * 5 +
+                                  [_i64, _i64, ctypes.c_float, ctypes.c_float, _c_void_p,
+                                   _c_void_p, _i64, _c_void_p]),
     "latentmoe_muon_create": (ctypes.c_int, [ctypes.POINTER(latentmoe_muon_dims),
                                              ctypes.POINTER(_c_void_p)]),
     "latentmoe_muon_orthogonalize": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _c_void_p,
@@ -303,6 +318,107 @@ class LatentMoE:
         check(load().latentmoe_lbl_stats(self.handle, ps.data_ptr(), cn.data_ptr(),
                                          _stream(stream)), "latentmoe_lbl_stats")
         return ps, cn
+
+    def _rows(self, t, name: str, T: int):
+        """Row stride of a [T, E] fp32 tensor whose columns are contiguous."""
+        import torch
+        _need(t.is_cuda and t.dtype == torch.float32 and
+              tuple(t.shape) == (T, self.dims.num_experts) and
+              (t.stride(1) == 1 or t.shape[1] == 1),
+              f"{name} must be a float32 CUDA tensor [{T}, {self.dims.num_experts}] with "
+              "contiguous rows")
+        return t.stride(0) if T > 1 else self.dims.num_experts
+
+    def _per_slot(self, t, name: str, T: int, dtype) -> None:
+        _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == (T, self.k) and
+              t.is_contiguous(),
+              f"{name} must be a contiguous {dtype} CUDA tensor [{T}, {self.k}]")
+
+    def _sequences(self, T: int, seq_len: int) -> int:
+        L = seq_len or T
+        _need(L > 0 and T > 0 and T % L == 0, "seq_len must divide the number of tokens")
+        return T // L
+
+    def _valid(self, valid, T: int):
+        import torch
+        if valid is None:
+            return None
+        _need(valid.is_cuda and valid.dtype in (torch.uint8, torch.bool) and valid.numel() == T and
+              valid.is_contiguous(), f"valid must be a contiguous uint8 or bool CUDA tensor [{T}]")
+        return valid.data_ptr()
+
+    def balance_loss(self, logits, idx, valid=None, seq_len: int = 0, balance_coef: float = 1.0,
+                     z_coef: float = 0.0, stream=None):
+        """The router's balance loss of logits [T, E] fp32 and choices idx
+        [T, k] int32: {"loss": [total, balance, z], "counts" [S, E] int32,
+        "prob_sum" [S, E], "z_sum" [S], "tokens" [S] int32} over S = T /
+        seq_len sequences (0: one)."""
+        import torch
+        T, E = logits.shape[0], self.dims.num_experts
+        ld = self._rows(logits, "logits", T)
+        self._per_slot(idx, "idx", T, torch.int32)
+        S = self._sequences(T, seq_len)
+        # one allocation: counts, tokens, prob_sum, z_sum, loss
+        ints = torch.empty((S * (E + 1),), dtype=torch.int32, device=logits.device)
+        flts = torch.empty((S * (E + 1) + 3,), dtype=torch.float32, device=logits.device)
+        ip, fp = ints.data_ptr(), flts.data_ptr()
+        n = 4 * S * E
+        st = latentmoe_balance_stats(ip, fp, fp + n, ip + n)
+        check(load().latentmoe_balance_loss(
+            self.handle, logits.data_ptr(), ld, idx.data_ptr(), self._valid(valid, T), T, seq_len,
+            balance_coef, z_coef, ctypes.byref(st), fp + n + 4 * S, _stream(stream)),
+            "latentmoe_balance_loss", self.handle)
+        counts, tokens = ints.split((S * E, S))
+        prob, z, loss = flts.split((S * E, S, 3))
+        return {"loss": loss, "counts": counts.view(S, E), "prob_sum": prob.view(S, E),
+                "z_sum": z, "tokens": tokens}
+
+    def balance_loss_from_stats(self, stats, balance_coef: float = 1.0, z_coef: float = 0.0,
+                                stream=None):
+        """loss [3] from (summed) stats as returned by balance_loss."""
+        import torch
+        c = stats["counts"]
+        S, E = c.shape[0], self.dims.num_experts
+        for name, shape, dt in (("counts", (S, E), torch.int32), ("prob_sum", (S, E), torch.float32),
+                                ("z_sum", (S,), torch.float32), ("tokens", (S,), torch.int32)):
+            t = stats[name]
+            _need(t.is_cuda and t.dtype == dt and tuple(t.shape) == shape and t.is_contiguous(),
+                  f"{name} must be a contiguous {dt} CUDA tensor {list(shape)}")
+        loss = torch.empty((3,), dtype=torch.float32, device=c.device)
+        st = latentmoe_balance_stats(*(stats[n].data_ptr() for n in
+                                       ("counts", "prob_sum", "z_sum", "tokens")))
+        check(load().latentmoe_balance_loss_from_stats(self.handle, ctypes.byref(st), S,
+                                                       balance_coef, z_coef, loss.data_ptr(),
+                                                       _stream(stream)),
+              "latentmoe_balance_loss_from_stats", self.handle)
+        return loss
+
+    def router_backward(self, logits, idx, counts, tokens, d_gates=None, valid=None,
+                        seq_len: int = 0, balance_coef: float = 1.0, z_coef: float = 0.0,
+                        d_loss=None, out=None, stream=None):
+        """d logits [T, E] fp32 of d_loss * loss[0] + sum d_gates * gates."""
+        import torch
+        T, E = logits.shape[0], self.dims.num_experts
+        ld = self._rows(logits, "logits", T)
+        S = self._sequences(T, seq_len)
+        if idx is not None:
+            self._per_slot(idx, "idx", T, torch.int32)
+        if d_gates is not None:
+            self._per_slot(d_gates, "d_gates", T, torch.float32)
+        for t, name, shape in ((counts, "counts", (S, E)), (tokens, "tokens", (S,))):
+            _need(t.is_cuda and t.dtype == torch.int32 and tuple(t.shape) == shape and
+                  t.is_contiguous(), f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
+        if d_loss is not None:
+            _need(d_loss.is_cuda and d_loss.dtype == torch.float32 and d_loss.numel() == 1,
+                  "d_loss must be one float32 on the GPU")
+        if out is None:
+            out = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        check(load().latentmoe_router_backward(
+            self.handle, logits.data_ptr(), ld, _ptr(idx), _ptr(d_gates), self._valid(valid, T),
+            counts.data_ptr(), tokens.data_ptr(), T, seq_len, balance_coef, z_coef, _ptr(d_loss),
+            out.data_ptr(), self._rows(out, "out", T), _stream(stream)),
+            "latentmoe_router_backward", self.handle)
+        return out
 
     def status(self) -> int:
         v = ctypes.c_uint32(0)

@@ -25,6 +25,7 @@
 // and both record their maxima for the scale update.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -36,6 +37,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "balance.h"
 #include "gemm_fused.cuh"
 #include "kernels.h"
 #include "latentmoe.h"
@@ -173,6 +175,7 @@ struct latentmoe {
   int* cbase = nullptr;
   int* counts = nullptr;
   float* lbl_partial = nullptr;
+  lmoe::BalanceScratch bal;     // scratch of latentmoe_balance_loss
   int* offsets = nullptr;
   int* perm = nullptr;
   int* pos = nullptr;
@@ -576,6 +579,10 @@ int latentmoe_create(const latentmoe_dims* dims, int top_k, uint32_t flags, late
   const size_t o_f8 = take(sizeof(lmoe::Fp8State));
   const size_t o_x8 = take(h->fp8_dense ? T * d.hidden : 16);
   const size_t o_y32 = take(h->fp8_dense && Fs > 0 ? T * d.hidden * 4 : 16);
+  const size_t bal_rows = 2 * static_cast<size_t>(h->sms);
+  const size_t o_bprob = take(bal_rows * E * 4), o_bcount = take(bal_rows * E * 4);
+  const size_t o_bz = take(bal_rows * 4), o_btok = take(bal_rows * 4);
+  const size_t o_bseq = take(2 * T * 4), o_bticket = take((bal_rows + 1) * 4);
   e = cudaMalloc(&h->ws, off);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -605,8 +612,16 @@ int latentmoe_create(const latentmoe_dims* dims, int top_k, uint32_t flags, late
   h->f8 = reinterpret_cast<lmoe::Fp8State*>(base + o_f8);
   h->x8 = reinterpret_cast<uint8_t*>(base + o_x8);
   h->y32 = reinterpret_cast<float*>(base + o_y32);
+  h->bal.prob = reinterpret_cast<float*>(base + o_bprob);
+  h->bal.count = reinterpret_cast<int*>(base + o_bcount);
+  h->bal.z = reinterpret_cast<float*>(base + o_bz);
+  h->bal.tokens = reinterpret_cast<int*>(base + o_btok);
+  h->bal.seq = reinterpret_cast<float*>(base + o_bseq);
+  h->bal.ticket = reinterpret_cast<unsigned*>(base + o_bticket);
+  h->bal.units = h->sms;
   e = cudaMemset(h->status, 0, 16);
   if (e == cudaSuccess) e = cudaMemset(h->tile_counter, 0, 16);
+  if (e == cudaSuccess) e = cudaMemset(h->bal.ticket, 0, (bal_rows + 1) * 4);
   if (e == cudaSuccess && h->dep) e = cudaMemset(h->dep, 0, E * (F / 256) * 4);
   if (e == cudaSuccess) {
     // delayed scaling starts with an empty history and unit scales
@@ -1251,6 +1266,111 @@ int latentmoe_lbl_stats(latentmoe_t h, float* prob_sum, int32_t* counts,
   if (counts)
     LMOE_CK(h, cudaMemcpyAsync(counts, h->counts, static_cast<size_t>(E) * 4,
                                cudaMemcpyDeviceToDevice, s));
+  return LATENTMOE_OK;
+}
+
+namespace {
+
+// Sizes shared by the balance loss and its backward: the sequences (seq_len 0:
+// one of T tokens) and the row stride (0: E). Returns a LATENTMOE_* code.
+int balance_sizes(const latentmoe* h, int64_t T, int64_t* seq_len, int64_t* ld) {
+  const int64_t E = h->dims.num_experts;
+  if (T < 1 || T > h->dims.max_tokens || *seq_len < 0) return LATENTMOE_ERR_INVALID_ARG;
+  if (*seq_len == 0) *seq_len = T;
+  if (T % *seq_len != 0) return LATENTMOE_ERR_INVALID_ARG;
+  if (*ld == 0) *ld = E;
+  if (*ld < E) return LATENTMOE_ERR_INVALID_ARG;
+  return LATENTMOE_OK;
+}
+
+}  // namespace
+
+int latentmoe_balance_loss(latentmoe_t h, const float* logits, int64_t ld, const int32_t* idx,
+                           const uint8_t* valid, int64_t T, int64_t seq_len, float balance_coef,
+                           float z_coef, const latentmoe_balance_stats* stats, float* loss,
+                           latentmoe_stream_t st) {
+  if (h == nullptr || logits == nullptr || idx == nullptr || stats == nullptr || loss == nullptr)
+    return LATENTMOE_ERR_INVALID_ARG;
+  if (stats->counts == nullptr || stats->prob_sum == nullptr || stats->z_sum == nullptr ||
+      stats->tokens == nullptr || !isfinite(balance_coef) || !isfinite(z_coef))
+    return LATENTMOE_ERR_INVALID_ARG;
+  const int rc = balance_sizes(h, T, &seq_len, &ld);
+  if (rc != LATENTMOE_OK) return rc;
+  if (!aligned16(logits)) return LATENTMOE_ERR_UNSUPPORTED;
+  LMOE_CK(h, cudaSetDevice(h->device));
+  lmoe::BalanceArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.idx = idx;
+  a.valid = valid;
+  a.seqs = static_cast<int>(T / seq_len);
+  a.seq_len = static_cast<int>(seq_len);
+  a.E = static_cast<int>(h->dims.num_experts);
+  a.k = h->k;
+  a.balance_coef = balance_coef;
+  a.z_coef = z_coef;
+  a.counts = stats->counts;
+  a.prob_sum = stats->prob_sum;
+  a.z_sum = stats->z_sum;
+  a.tokens = stats->tokens;
+  a.loss = loss;
+  a.status = h->status;
+  LMOE_CK(h, lmoe::launch_balance_loss(a, h->bal, reinterpret_cast<cudaStream_t>(st)));
+  h->launches += 1;
+  return LATENTMOE_OK;
+}
+
+int latentmoe_balance_loss_from_stats(latentmoe_t h, const latentmoe_balance_stats* stats,
+                                      int64_t sequences, float balance_coef, float z_coef,
+                                      float* loss, latentmoe_stream_t st) {
+  if (h == nullptr || stats == nullptr || loss == nullptr) return LATENTMOE_ERR_INVALID_ARG;
+  if (stats->counts == nullptr || stats->prob_sum == nullptr || stats->z_sum == nullptr ||
+      stats->tokens == nullptr || !isfinite(balance_coef) || !isfinite(z_coef))
+    return LATENTMOE_ERR_INVALID_ARG;
+  if (sequences < 1 || sequences > h->dims.max_tokens) return LATENTMOE_ERR_INVALID_ARG;
+  LMOE_CK(h, cudaSetDevice(h->device));
+  LMOE_CK(h, lmoe::launch_balance_from_stats(
+                 stats->counts, stats->prob_sum, stats->z_sum, stats->tokens,
+                 static_cast<int>(sequences), static_cast<int>(h->dims.num_experts), h->k,
+                 balance_coef, z_coef, loss, reinterpret_cast<cudaStream_t>(st)));
+  h->launches += 1;
+  return LATENTMOE_OK;
+}
+
+int latentmoe_router_backward(latentmoe_t h, const float* logits, int64_t ld, const int32_t* idx,
+                              const float* d_gates, const uint8_t* valid, const int32_t* counts,
+                              const int32_t* tokens, int64_t T, int64_t seq_len,
+                              float balance_coef, float z_coef, const float* d_loss,
+                              float* d_logits, int64_t ldd, latentmoe_stream_t st) {
+  if (h == nullptr || logits == nullptr || counts == nullptr || tokens == nullptr ||
+      d_logits == nullptr || (d_gates != nullptr && idx == nullptr))
+    return LATENTMOE_ERR_INVALID_ARG;
+  if (!isfinite(balance_coef) || !isfinite(z_coef)) return LATENTMOE_ERR_INVALID_ARG;
+  int rc = balance_sizes(h, T, &seq_len, &ld);
+  if (rc == LATENTMOE_OK) rc = balance_sizes(h, T, &seq_len, &ldd);
+  if (rc != LATENTMOE_OK) return rc;
+  if (!aligned16(logits) || !aligned16(d_logits)) return LATENTMOE_ERR_UNSUPPORTED;
+  LMOE_CK(h, cudaSetDevice(h->device));
+  lmoe::RouterBackwardArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.idx = idx;
+  a.d_gates = d_gates;
+  a.valid = valid;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.d_loss = d_loss;
+  a.seqs = static_cast<int>(T / seq_len);
+  a.seq_len = static_cast<int>(seq_len);
+  a.E = static_cast<int>(h->dims.num_experts);
+  a.k = h->k;
+  a.renorm = (h->flags & LATENTMOE_RENORM) != 0;
+  a.balance_coef = balance_coef;
+  a.z_coef = z_coef;
+  a.d_logits = d_logits;
+  a.ldd = ldd;
+  LMOE_CK(h, lmoe::launch_router_backward(a, h->sms, reinterpret_cast<cudaStream_t>(st)));
+  h->launches += 1;
   return LATENTMOE_OK;
 }
 

@@ -1,0 +1,596 @@
+// The router's balance loss with per-expert counts, and its backward pass
+// together with that of the gates.
+//
+// "The Training and RL Infrastructure Behind MAI-Thinking-1", section
+// "Sharding and parallelism": a global-batch load-balancing loss; "Frontier
+// Pre-training at Microsoft AI", section "Reducing per-expert overhead".
+// Neither gives a formula; this is the usual product of load and mean
+// probability, per sequence s of L tokens of which N_s count:
+//   balance_s = E / (k N_s^2) sum_e counts[s,e] sum_t p[t,e]
+//   z_s       = 1 / N_s sum_t lse_t^2,   lse_t = log sum_e exp(logit[t,e])
+//   loss      = mean_s (balance_coef balance_s + z_coef z_s)
+// The counts are integers, so only p and lse carry gradients:
+//   d logit[t,e] = p_e (w_e - sum_f w_f p_f + q lse)   tokens that count
+//                + the gates' part (see router_backward_kernel)
+//   w_e = balance_coef E / (S k N_s^2) counts[s,e],  q = 2 z_coef / (S N_s)
+//
+// Both passes read the logits once (a row lives in the registers of the lanes
+// that share it: softmax, sums and outputs need no second read) and are bound
+// by memory traffic for large batches, by launch latency for small ones.
+// Rows: LANES lanes of a warp hold one row, NV float4 a lane (E <= LANES NV 4),
+// so a warp works on 32 / LANES rows at a time, U of those in flight.
+// All sums over tokens are fp32 in a fixed order: lanes, warps, CTAs, groups
+// of CTAs (integers may be added in any order).
+#include <math.h>
+
+#include "balance.h"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace lmoe {
+
+namespace {
+
+constexpr int kBalThreads = 1024;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalGroup = 16;  // CTAs whose partial sums one CTA adds
+constexpr int kBackThreads = 512;
+
+// How a row of E logits lies in a warp's registers.
+template <int LANES_, int NV_, bool VEC_>
+struct Row {
+  static constexpr int LANES = LANES_;
+  static constexpr int NV = NV_;
+  static constexpr bool VEC = VEC_;
+  static constexpr int N = 4 * NV;              // elements a lane
+  static constexpr int ROWS = 32 / LANES;       // rows of a warp at once
+  static constexpr int U = NV >= 3 ? 1 : 4 / NV;  // of those in flight
+  static constexpr int BATCH = ROWS * U;
+  static constexpr int WIDTH = LANES * N;       // columns covered, >= E
+  // column of element i of lane q
+  __device__ static __forceinline__ int col(int q, int i) {
+    return VEC ? 4 * (q + LANES * (i >> 2)) + (i & 3) : q + LANES * i;
+  }
+  __device__ static __forceinline__ void load(const float* row, int q, int E, float (&x)[N]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = 4 * (q + LANES * v);
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (c < E) f = *reinterpret_cast<const float4*>(row + c);  // E % 4 == 0
+        x[4 * v] = f.x;
+        x[4 * v + 1] = f.y;
+        x[4 * v + 2] = f.z;
+        x[4 * v + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = q + LANES * i;
+        x[i] = c < E ? row[c] : -INFINITY;
+      }
+    }
+  }
+  __device__ static __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ static __forceinline__ float max(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+};
+
+// x <- exp(x - max) over the row; returns the sum, and the max in m. A row of
+// -inf alone gives sum 0 (and max 0); a NaN makes the sum NaN.
+template <class R>
+__device__ __forceinline__ float row_exp(float (&x)[R::N], float& m) {
+  m = x[0];
+#pragma unroll
+  for (int i = 1; i < R::N; ++i) m = fmaxf(m, x[i]);
+  m = R::max(m);
+  if (m == -INFINITY) m = 0.0f;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R::N; ++i) {
+    x[i] = __expf(x[i] - m);
+    s += x[i];
+  }
+  return R::sum(s);
+}
+
+// Fixed-order sum over the block; every thread gets it. `buf`: kBalWarps floats.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) buf[warp] = v;
+  __syncthreads();
+  float t = buf[lane];  // kBalWarps == 32
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+// True in every thread of the CTA that arrives last of `n` at *ticket; the
+// others' global writes before their arrival are visible to it. The last one
+// leaves the ticket at zero.
+__device__ __forceinline__ bool arrive_last(unsigned* ticket, unsigned n, int* flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned old = atomicAdd(ticket, 1u);
+    *flag = old == n - 1;
+    if (old == n - 1) *ticket = 0;
+  }
+  __syncthreads();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+__device__ __forceinline__ void store_loss(float* loss, float balance, float z, float bc,
+                                           float zc) {
+  loss[0] = bc * balance + zc * z;
+  loss[1] = balance;
+  loss[2] = z;
+}
+
+}  // namespace
+
+// Unit u: part u % parts of sequence u / parts. With one part a sequence the
+// CTA has the sequence's sums itself; otherwise the last CTA of each group of
+// kBalGroup parts adds the group's, and the last group of the sequence adds
+// the groups'. The last sequence adds the sequences' losses.
+template <class R>
+__global__ void __launch_bounds__(kBalThreads, 1)
+    balance_loss_kernel(const BalanceArgs a, const BalanceScratch w, int parts, int part_rows) {
+  extern __shared__ float red[];  // [kBalWarps][E] column sums
+  __shared__ int hist[512];
+  __shared__ float warp_z[kBalWarps];
+  __shared__ int warp_n[kBalWarps];
+  __shared__ float buf[kBalWarps];
+  __shared__ int flag;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = lane % R::LANES, sub = lane / R::LANES;
+  const int E = a.E, k = a.k;
+  const int units = a.seqs * parts;
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int s = unit / parts, part = unit - s * parts;
+    for (int e = threadIdx.x; e < E; e += kBalThreads) hist[e] = 0;
+    __syncthreads();
+    const int r0 = part * part_rows;
+    const int r1 = min(a.seq_len, r0 + part_rows);
+    const long long t0 = static_cast<long long>(s) * a.seq_len;
+    float acc[R::N];
+#pragma unroll
+    for (int i = 0; i < R::N; ++i) acc[i] = 0.0f;
+    float zsum = 0.0f;
+    int ntok = 0;
+    bool bad = false;
+    for (int base = r0 + warp * R::BATCH; base < r1; base += kBalWarps * R::BATCH) {
+      float x[R::U][R::N];
+      bool in[R::U];
+#pragma unroll
+      for (int u = 0; u < R::U; ++u) {
+        const int r = base + u * R::ROWS + sub;
+        const long long t = t0 + r;
+        in[u] = r < r1;
+        // a row past the part is read as the batch's first row (in range) and dropped
+        R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, E, x[u]);
+        if (in[u] && a.valid != nullptr) in[u] = a.valid[t] != 0;
+      }
+#pragma unroll
+      for (int u = 0; u < R::U; ++u) {
+        const long long t = t0 + base + u * R::ROWS + sub;
+        float m;
+        const float sum = row_exp<R>(x[u], m);
+        const bool ok = in[u] && !(sum == 0.0f);
+        const float inv = 1.0f / sum;
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < R::N; ++i) acc[i] = fmaf(x[u][i], inv, acc[i]);
+          if (q == 0) {
+            const float lse = m + logf(sum);
+            zsum = fmaf(lse, lse, zsum);
+            ntok += 1;
+          }
+          for (int j = q; j < k; j += R::LANES) {
+            const int id = a.idx[t * k + j];
+            if (static_cast<unsigned>(id) < static_cast<unsigned>(E))
+              atomicAdd(&hist[id], 1);
+            else
+              bad = true;
+          }
+        }
+      }
+    }
+    if (bad) atomicOr(a.status, kStatusBadExpert);
+    // lanes of other rows, then warps
+#pragma unroll
+    for (int o = R::LANES; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      zsum += __shfl_xor_sync(0xffffffffu, zsum, o);
+      ntok += __shfl_xor_sync(0xffffffffu, ntok, o);
+    }
+    if (sub == 0) {
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) {
+        const int c = R::col(q, i);
+        if (c < E) red[warp * E + c] = acc[i];
+      }
+    }
+    if (lane == 0) {
+      warp_z[warp] = zsum;
+      warp_n[warp] = ntok;
+    }
+    __syncthreads();
+    // thread e owns expert e from here on (E <= 512 < kBalThreads)
+    const int e = threadIdx.x;
+    float prob = 0.0f, z = 0.0f;
+    int count = 0, n = 0;
+    if (e < E) {
+#pragma unroll 8
+      for (int v = 0; v < kBalWarps; ++v) prob += red[v * E + e];
+      count = hist[e];
+    }
+    for (int v = 0; v < kBalWarps; ++v) {
+      z += warp_z[v];
+      n += warp_n[v];
+    }
+    bool mine = true;  // this CTA holds the sequence's totals
+    if (parts > 1) {
+      const int groups = (parts + kBalGroup - 1) / kBalGroup;
+      const int g = part / kBalGroup;
+      int rows = min(kBalGroup, parts - g * kBalGroup);  // partial sums to add
+      int first = s * parts + g * kBalGroup;
+      int at = unit;
+      unsigned* ticket = w.ticket + s * groups + g;
+      // twice at most: the group's parts, then the sequence's groups
+      for (int level = 0; level < 2 && mine; ++level) {
+        if (rows > 1) {
+          if (e < E) {
+            w.prob[static_cast<long long>(at) * E + e] = prob;
+            w.count[static_cast<long long>(at) * E + e] = count;
+          }
+          if (e == 0) {
+            w.z[at] = z;
+            w.tokens[at] = n;
+          }
+          mine = arrive_last(ticket, static_cast<unsigned>(rows), &flag);
+          if (mine) {
+            prob = z = 0.0f;
+            count = n = 0;
+#pragma unroll 4
+            for (int v = 0; v < rows; ++v) {
+              const long long from = first + v;
+              if (e < E) {
+                prob += __ldcg(w.prob + from * E + e);
+                count += __ldcg(w.count + from * E + e);
+              }
+              z += __ldcg(w.z + from);
+              n += __ldcg(w.tokens + from);
+            }
+          }
+        }
+        rows = groups;
+        first = w.units + s * groups;
+        at = first + g;
+        ticket = w.ticket + w.units + s;
+      }
+    }
+    if (mine) {
+      const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+      float term = 0.0f;
+      if (e < E) {
+        a.counts[static_cast<long long>(s) * E + e] = count;
+        a.prob_sum[static_cast<long long>(s) * E + e] = prob;
+        if (n > 0) term = (static_cast<float>(count) * inv) * (prob * inv);
+      }
+      const float balance =
+          block_sum(term, buf) * (static_cast<float>(E) / static_cast<float>(k));
+      const float zmean = n > 0 ? z * inv : 0.0f;
+      if (e == 0) {
+        a.z_sum[s] = z;
+        a.tokens[s] = n;
+      }
+      if (a.seqs == 1) {
+        if (e == 0) store_loss(a.loss, balance, zmean, a.balance_coef, a.z_coef);
+      } else {
+        if (e == 0) {
+          w.seq[2ll * s] = balance;
+          w.seq[2ll * s + 1] = zmean;
+        }
+        if (arrive_last(w.ticket + 2 * w.units, static_cast<unsigned>(a.seqs), &flag)) {
+          float bs = 0.0f, zs = 0.0f;
+          for (int i = threadIdx.x; i < a.seqs; i += kBalThreads) {
+            bs += __ldcg(w.seq + 2ll * i);
+            zs += __ldcg(w.seq + 2ll * i + 1);
+          }
+          bs = block_sum(bs, buf) / static_cast<float>(a.seqs);
+          zs = block_sum(zs, buf) / static_cast<float>(a.seqs);
+          if (e == 0) store_loss(a.loss, bs, zs, a.balance_coef, a.z_coef);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Sums of other ranks or micro-batches added: one CTA, a warp per sequence.
+__global__ void __launch_bounds__(kBalThreads)
+    balance_from_stats_kernel(const int* counts, const float* prob_sum, const float* z_sum,
+                              const int* tokens, int seqs, int E, int k, float bc, float zc,
+                              float* loss) {
+  __shared__ float buf[kBalWarps];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float bs = 0.0f, zs = 0.0f;
+  for (int s = warp; s < seqs; s += kBalWarps) {
+    const int n = tokens[s];
+    if (n <= 0) continue;
+    const float inv = 1.0f / static_cast<float>(n);
+    for (int e = lane; e < E; e += 32) {
+      const long long at = static_cast<long long>(s) * E + e;
+      bs = fmaf(static_cast<float>(counts[at]) * inv, prob_sum[at] * inv, bs);
+    }
+    if (lane == 0) zs = fmaf(z_sum[s], inv, zs);
+  }
+  bs = block_sum(bs, buf) * (static_cast<float>(E) / static_cast<float>(k)) /
+       static_cast<float>(seqs);
+  zs = block_sum(zs, buf) / static_cast<float>(seqs);
+  if (threadIdx.x == 0) store_loss(loss, bs, zs, bc, zc);
+}
+
+// d_logits. The gates' part, with D = sum_j g_j dg_j over the token's choices:
+//   g_j = p[idx_j]:            sum_{j: idx_j = e} g_j dg_j  -  p_e D
+//   g_j = p[idx_j] / sum_i p[idx_i], i.e. a softmax over the chosen logits
+//   alone (evaluated as that: no quotient of underflowed probabilities):
+//                              sum_{j: idx_j = e} g_j (dg_j - D)
+// The lanes of a row own one choice each, put its term into the warp's shared
+// row (zero between rows) and every lane picks up its own columns there.
+template <class R, bool GATES>
+__global__ void __launch_bounds__(kBackThreads)
+    router_backward_kernel(const RouterBackwardArgs a, int parts, int part_rows) {
+  extern __shared__ float sparse_all[];  // [warps][U][ROWS][WIDTH]
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = lane % R::LANES, sub = lane / R::LANES;
+  const int E = a.E, k = a.k;
+  float* sparse = sparse_all + warp * (R::U * R::ROWS * R::WIDTH);
+  if (GATES) {
+    for (int i = lane; i < R::U * R::ROWS * R::WIDTH; i += 32) sparse[i] = 0.0f;
+    __syncwarp();
+  }
+  const int s = blockIdx.x / parts, part = blockIdx.x - s * parts;
+  const int r0 = part * part_rows;
+  const int r1 = min(a.seq_len, r0 + part_rows);
+  const long long t0 = static_cast<long long>(s) * a.seq_len;
+  // w_e = c counts[s,e]; q lse: zq lse
+  const int n = a.tokens[s];
+  const float up = (a.d_loss != nullptr ? *a.d_loss : 1.0f) / static_cast<float>(a.seqs);
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+  const float wc =
+      up * a.balance_coef * (static_cast<float>(E) / static_cast<float>(k)) * inv_n * inv_n;
+  const float zq = up * 2.0f * a.z_coef * inv_n;
+  float wt[R::N];
+#pragma unroll
+  for (int i = 0; i < R::N; ++i) {
+    const int c = R::col(q, i);
+    wt[i] = c < E ? wc * static_cast<float>(a.counts[static_cast<long long>(s) * E + c]) : 0.0f;
+  }
+  for (int base = r0 + warp * R::BATCH; base < r1; base += (kBackThreads / 32) * R::BATCH) {
+    float x[R::U][R::N];
+    bool in[R::U], counted[R::U];
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int r = base + u * R::ROWS + sub;
+      const long long t = t0 + r;
+      in[u] = r < r1;
+      counted[u] = in[u];
+      R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, E, x[u]);
+      if (in[u] && a.valid != nullptr) counted[u] = a.valid[t] != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const long long t = t0 + base + u * R::ROWS + sub;
+      float m;
+      const float sum = row_exp<R>(x[u], m);
+      const bool empty = sum == 0.0f;
+      const float inv = empty ? 0.0f : 1.0f / sum;
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) dot = fmaf(x[u][i], wt[i], dot);
+      dot = R::sum(dot) * inv;
+      // p_e (wt_e + shift)
+      const bool on = counted[u] && !empty;
+      float shift = on ? fmaf(zq, m + logf(sum), -dot) : 0.0f;
+      float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
+      if constexpr (GATES) {
+        const float* row = a.logits + t * a.ld;
+        // the choices' logits; D; for the renormalised form their own max and sum
+        float best = -INFINITY;
+        if (a.renorm) {
+          for (int j = q; j < k; j += R::LANES) {
+            const int id = in[u] ? a.idx[t * k + j] : -1;
+            if (static_cast<unsigned>(id) < static_cast<unsigned>(E)) best = fmaxf(best, row[id]);
+          }
+          best = R::max(best);
+          if (best == -INFINITY) best = 0.0f;
+        }
+        float gs = 0.0f, gd = 0.0f;
+        for (int j = q; j < k; j += R::LANES) {
+          const int id = in[u] ? a.idx[t * k + j] : -1;
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(E)) {
+            const float g = a.renorm ? __expf(row[id] - best) : __expf(row[id] - m) * inv;
+            gs += g;
+            gd = fmaf(g, a.d_gates[t * k + j], gd);
+          }
+        }
+        gd = R::sum(gd);
+        float ginv = 1.0f;
+        if (a.renorm) {
+          gs = R::sum(gs);
+          ginv = gs == 0.0f ? 0.0f : 1.0f / gs;
+          gd *= ginv;
+        } else {
+          shift -= gd;
+        }
+        // whole warp: k / LANES rounds, one choice a lane
+        for (int j0 = 0; j0 < k; j0 += R::LANES) {
+          const int j = j0 + q;
+          const int id = in[u] && j < k ? a.idx[t * k + j] : -1;
+          const bool has = static_cast<unsigned>(id) < static_cast<unsigned>(E);
+          float v = 0.0f;
+          if (has) {
+            const float dg = a.d_gates[t * k + j];
+            v = a.renorm ? __expf(row[id] - best) * ginv * (dg - gd)
+                         : __expf(row[id] - m) * inv * dg;
+          }
+          // a token's choices differ as a rule; given choices may repeat, and
+          // then their terms are added in the order of the choices
+          const unsigned same = __match_any_sync(0xffffffffu, has ? sub * 1024 + id : -1 - lane);
+          if (__all_sync(0xffffffffu, __popc(same) == 1)) {
+            if (has) mine[id] += v;
+          } else {
+            for (int o = 0; o < R::LANES; ++o) {
+              if (has && q == o) mine[id] += v;
+              __syncwarp();
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // a token that does not count gets zeros (whatever its logits hold) or
+      // the gates' part alone
+      float d[R::N];
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) {
+        const float v = (x[u][i] * inv) * (on ? wt[i] + shift : shift);
+        d[i] = GATES || on ? v : 0.0f;
+      }
+      if constexpr (GATES) {
+#pragma unroll
+        for (int i = 0; i < R::N; ++i) {
+          const int c = R::col(q, i);
+          d[i] += mine[c];
+          mine[c] = 0.0f;
+        }
+        __syncwarp();
+      }
+      if (in[u]) {
+        float* out = a.d_logits + t * a.ldd;
+        if constexpr (R::VEC) {
+#pragma unroll
+          for (int v = 0; v < R::NV; ++v) {
+            const int c = 4 * (q + R::LANES * v);
+            if (c < E)
+              *reinterpret_cast<float4*>(out + c) =
+                  make_float4(d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < R::N; ++i) {
+            const int c = q + R::LANES * i;
+            if (c < E) out[c] = d[i];
+          }
+        }
+      }
+    }
+  }
+}
+
+namespace {
+
+int div_up(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+template <class R>
+cudaError_t loss_impl(const BalanceArgs& a, const BalanceScratch& w, cudaStream_t s) {
+  const int smem = kBalWarps * a.E * 4;
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        balance_loss_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBalWarps * 512 * 4);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  // parts of a sequence: as many CTAs as there are for each, no more than give
+  // every warp a batch of rows
+  int parts = w.units / a.seqs;
+  const int most = div_up(a.seq_len, kBalWarps * R::BATCH);
+  if (parts > most) parts = most;
+  if (parts < 1) parts = 1;
+  const int part_rows = div_up(a.seq_len, parts);
+  parts = div_up(a.seq_len, part_rows);
+  const long long units = static_cast<long long>(a.seqs) * parts;
+  const int grid = static_cast<int>(units < w.units ? units : w.units);
+  return launch_kernel(balance_loss_kernel<R>, dim3(grid), dim3(kBalThreads), smem, s, 1, false, a,
+                       w, parts, part_rows);
+}
+
+template <class R, bool GATES>
+cudaError_t backward_impl(const RouterBackwardArgs& a, int sms, cudaStream_t s) {
+  constexpr int warps = kBackThreads / 32;
+  const int smem = GATES ? warps * R::U * R::ROWS * R::WIDTH * 4 : 0;
+  // a CTA's rows: two batches a warp, or more once every SM has eight CTAs
+  const long long T = static_cast<long long>(a.seqs) * a.seq_len;
+  long long rows = 2ll * warps * R::BATCH;
+  const long long fill = (T + 8ll * sms - 1) / (8ll * sms);
+  if (rows < fill) rows = fill;
+  int parts = div_up(a.seq_len, rows);
+  const int part_rows = div_up(a.seq_len, parts);
+  parts = div_up(a.seq_len, part_rows);
+  return launch_kernel(router_backward_kernel<R, GATES>,
+                       dim3(static_cast<unsigned>(a.seqs) * static_cast<unsigned>(parts)),
+                       dim3(kBackThreads), smem, s, 1, false, a, parts, part_rows);
+}
+
+// The layout for E experts: the fewest lanes that hold a row in one float4
+// each, then more float4 a lane.
+template <bool VEC, class F>
+cudaError_t with_row(int E, const F& f) {
+  if (E <= 16) return f(Row<4, 1, VEC>());
+  if (E <= 32) return f(Row<8, 1, VEC>());
+  if (E <= 64) return f(Row<16, 1, VEC>());
+  if (E <= 128) return f(Row<32, 1, VEC>());
+  if (E <= 256) return f(Row<32, 2, VEC>());
+  if (E <= 384) return f(Row<32, 3, VEC>());
+  return f(Row<32, 4, VEC>());
+}
+
+}  // namespace
+
+cudaError_t launch_balance_loss(const BalanceArgs& a, const BalanceScratch& w, cudaStream_t s) {
+  const auto go = [&](auto r) { return loss_impl<decltype(r)>(a, w, s); };
+  // float4 loads: rows that start on 16 bytes and end on whole vectors
+  return a.E % 4 == 0 && a.ld % 4 == 0 ? with_row<true>(a.E, go) : with_row<false>(a.E, go);
+}
+
+cudaError_t launch_balance_from_stats(const int* counts, const float* prob_sum, const float* z_sum,
+                                      const int* tokens, int seqs, int E, int k,
+                                      float balance_coef, float z_coef, float* loss,
+                                      cudaStream_t s) {
+  return launch_kernel(balance_from_stats_kernel, dim3(1), dim3(kBalThreads), 0, s, 1, false,
+                       counts, prob_sum, z_sum, tokens, seqs, E, k, balance_coef, z_coef, loss);
+}
+
+cudaError_t launch_router_backward(const RouterBackwardArgs& a, int sms, cudaStream_t s) {
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && a.ldd % 4 == 0;
+  if (a.d_gates != nullptr) {
+    const auto go = [&](auto r) { return backward_impl<decltype(r), true>(a, sms, s); };
+    return vec ? with_row<true>(a.E, go) : with_row<false>(a.E, go);
+  }
+  const auto go = [&](auto r) { return backward_impl<decltype(r), false>(a, sms, s); };
+  return vec ? with_row<true>(a.E, go) : with_row<false>(a.E, go);
+}
+
+}  // namespace lmoe

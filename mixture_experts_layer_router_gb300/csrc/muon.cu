@@ -6,8 +6,8 @@
 // Microsoft's 2.8T base model, and whether its compute numbers add up"; the
 // iteration is the published quintic one.
 //
-// Launches of one call: norm, init, then gram, poly, apply for every step;
-// the last apply writes the caller's output or weights.
+// Launches of one call: norm, init, and the iteration, whose last product
+// writes the caller's output or weights.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -25,17 +25,12 @@ using lmoe::NsArgs;
 
 namespace {
 
-constexpr int kMaxSteps = 32;
+using lmoe::kNsMaxSteps;
 constexpr long long kMaxSide = 65536;
 // fp16 entries are kept at or below 2^14, a quarter of the format's range
 constexpr double kHalfTop = 16384.0;
-
-// Per step: coefficients and the power-of-two scales of the fp16 X, A and
-// P = b A + c A^2.
-struct Step {
-  float a, b, c;
-  float sx, sa, sp;
-};
+// matrices in flight at once: their X (fp32 and fp16 twice), A and P
+constexpr long long kGroupBytes = 320ll << 20;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -47,20 +42,24 @@ float pow2_scale(double bound) {
   return static_cast<float>(ldexp(1.0, e));
 }
 
-// 3-D fp16 map (cols, rows, batch) with row stride ld, boxes of 64 x 64 x 1,
-// 128-byte swizzle, zeros outside.
+// 3-D fp16 (or fp32) map (cols, rows, batch) with row stride ld, zeros outside;
+// boxes of `box` columns x `box` rows. Swizzle: as wide as a box row, 64 or 128
+// bytes.
 bool make_ns_map(CUtensorMap* map, const void* p, long long batch, long long rows, long long cols,
-                 long long ld) {
+                 long long ld, int box, bool f32 = false) {
   const lmoe::EncodeTiledFn fn = lmoe::tensor_map_encoder();
   if (fn == nullptr) return false;
+  const int size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
-                                 static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint64_t strides[2] = {
+      static_cast<cuuint64_t>(ld) * size,
+      static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * size};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -72,20 +71,18 @@ struct latentmoe_muon {
   bool tall = false;
   int steps = 0;
   float eps = 0.0f;
-  Step step[kMaxSteps];
+  float scale0 = 1.0f;  // of the first X
   int device = 0;
   int sms = 1;
-  long long ldx = 0, lda = 0;
+  int group = 1;        // matrices in flight
   int chunks = 1;
   long long chunk = 0;
   void* ws = nullptr;
-  float* x32 = nullptr;
-  __half* x16[2] = {nullptr, nullptr};
-  __half* gram = nullptr;
-  __half* poly = nullptr;
   float* partial = nullptr;
-  unsigned* status = nullptr;
-  CUtensorMap m_x[2], m_gram, m_poly;
+  float* x32 = nullptr;   // [batch, rows, ld_x]
+  __half* x16 = nullptr;  // the first X
+  NsArgs args;  // everything but the output and the tile shape
+  lmoe::NsMaps maps;
   int pairs = 2;  // 0 single SMs, 1 SM pairs, 2 by the number of tiles
   int64_t launches = 0;
   int last_cuda = 0;
@@ -104,38 +101,27 @@ int fail(latentmoe_muon* h, cudaError_t e) {
     if (e_ != cudaSuccess) return fail(h, e_);  \
   } while (0)
 
-long long tiles_of(long long M, long long N, long long bt, bool sym) {
-  const long long mt = (M + bt - 1) / bt, nt = (N + bt - 1) / bt;
-  return sym ? mt * (mt + 1) / 2 : mt * nt;
+long long sym_tiles(long long m, long long bt) {
+  const long long t = (m + bt - 1) / bt;
+  return t * (t + 1) / 2;
+}
+long long tiles(long long M, long long N, long long bt) {
+  return ((M + bt - 1) / bt) * ((N + bt - 1) / bt);
 }
 
-// SM pairs (256 x 256 tiles) or single SMs (128 x 128): whichever needs fewer
-// rounds of tiles, a pair tile being two single tiles' work per SM.
-bool use_pairs(const latentmoe_muon* h, long long M, long long N, bool sym) {
+// SM pairs (256 x 256 tiles) or single SMs (128 x 128)? A single tile's k-block
+// takes about as long as a pair tile's once all SMs run (both are then bound by
+// operand traffic from L2; 560 and 600 clocks measured), so the fewer rounds of
+// tiles decide, weighted with the k-blocks of each product.
+bool use_pairs(const latentmoe_muon* h) {
   if (h->pairs != 2) return h->pairs == 1;
-  const long long tp = tiles_of(M, N, 256, sym) * h->batch;
-  const long long ts = tiles_of(M, N, 128, sym) * h->batch;
-  const long long np = h->sms / 2 > 0 ? h->sms / 2 : 1;
-  const long long rounds_p = (tp + np - 1) / np, rounds_s = (ts + h->sms - 1) / h->sms;
-  return 2 * rounds_p <= rounds_s;
-}
-
-int product(latentmoe_muon* h, int epi, const CUtensorMap& ma, const CUtensorMap& mb, long long M,
-            long long N, long long K, NsArgs a, cudaStream_t s) {
-  const bool sym = epi != lmoe::kNsApply;
-  const bool pair = use_pairs(h, M, N, sym);
-  const long long bt = pair ? 256 : 128;
-  a.batch = static_cast<int>(h->batch);
-  a.M = static_cast<int>(M);
-  a.N = static_cast<int>(N);
-  a.k_blocks = static_cast<int>((K + lmoe::kNsBK - 1) / lmoe::kNsBK);
-  a.m_tiles = static_cast<int>((M + bt - 1) / bt);
-  a.n_tiles = static_cast<int>((N + bt - 1) / bt);
-  a.tiles = static_cast<int>(tiles_of(M, N, bt, sym));
-  a.status = h->status;
-  NS_CK(h, lmoe::launch_ns_gemm(epi, h->tall, pair, ma, mb, a, h->sms, s));
-  h->launches += 1;
-  return LATENTMOE_OK;
+  const long long m = h->side, n = h->tall ? h->rows : h->cols;
+  const auto rounds = [&](long long bt, long long units) {
+    const long long sym = (sym_tiles(m, bt) * h->batch + units - 1) / units;
+    const long long app = (tiles(m, n, bt) * h->batch + units - 1) / units;
+    return sym * (n + m) + app * m;
+  };
+  return h->sms >= 2 && rounds(256, h->sms / 2) < rounds(128, h->sms);
 }
 
 // The whole iteration on U; the last product writes `out` as out_mode says.
@@ -143,48 +129,23 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
             float move, cudaStream_t s) {
   const lmoe::PdlScope pdl(true);
   const long long n = h->rows * h->cols;
+  NsArgs& a = h->args;
   NS_CK(h, lmoe::launch_ns_norm(u, h->batch, n, h->chunks, h->chunk, h->partial, s));
-  NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, h->ldx, h->chunks, h->partial,
-                                h->eps, h->step[0].sx, h->x32, h->x16[0], s));
+  NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, a.ld_x, h->chunks, h->partial,
+                                h->eps, h->scale0, h->x32, h->x16, a.done, 3 * a.steps, a.counter, s));
   h->launches += 2;
-  const long long m = h->side;
-  for (int i = 0; i < h->steps; ++i) {
-    const Step& st = h->step[i];
-    const bool last = i + 1 == h->steps;
-    const CUtensorMap& mx = h->m_x[i & 1];
-    NsArgs a;
-    memset(&a, 0, sizeof(a));
-    a.ld = h->lda;
-    a.bstride = m * h->lda;
-    // A, scaled by sa, from X scaled by sx
-    a.alpha = st.sa / (st.sx * st.sx);
-    a.out16 = h->gram;
-    int r = product(h, lmoe::kNsGram, mx, mx, m, m, h->tall ? h->rows : h->cols, a, s);
-    if (r != LATENTMOE_OK) return r;
-    // P = b A + c A^2, scaled by sp
-    a.alpha = st.c * st.sp / (st.sa * st.sa);
-    a.beta = st.b * st.sp / st.sa;
-    a.out16 = h->poly;
-    a.old16 = h->gram;
-    r = product(h, lmoe::kNsPoly, h->m_gram, h->m_gram, m, m, m, a, s);
-    if (r != LATENTMOE_OK) return r;
-    // X <- a X + P X (wide) or a X + X P (tall)
-    a.alpha = 1.0f / (st.sp * st.sx);
-    a.beta = st.a;
-    a.scale = last ? 1.0f : h->step[i + 1].sx;
-    a.out16 = h->x16[(i + 1) & 1];
-    a.old16 = nullptr;
-    a.x32 = h->x32;
-    a.ld = h->ldx;
-    a.bstride = h->rows * h->ldx;
-    a.out_mode = last ? out_mode : static_cast<int>(lmoe::kNsOutNext);
-    a.out = out;
-    a.keep = keep;
-    a.move = move;
-    r = product(h, lmoe::kNsApply, h->tall ? mx : h->m_poly, h->tall ? h->m_poly : mx, h->rows,
-                h->cols, m, a, s);
-    if (r != LATENTMOE_OK) return r;
-  }
+  const bool pair = use_pairs(h);
+  const long long bt = pair ? 256 : 128;
+  a.sym_tiles = static_cast<int>(sym_tiles(h->side, bt));
+  a.m_tiles = static_cast<int>((h->rows + bt - 1) / bt);
+  a.apply_tiles = static_cast<int>(tiles(h->rows, h->cols, bt));
+  a.group = h->group;
+  a.out_mode = out_mode;
+  a.out = out;
+  a.keep = keep;
+  a.move = move;
+  NS_CK(h, lmoe::launch_ns_iterate(pair, h->maps, a, h->sms, s));
+  h->launches += 1;
   return LATENTMOE_OK;
 }
 
@@ -199,41 +160,57 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   const latentmoe_muon_dims d = *dims;
   if (d.batch < 1 || d.rows < 1 || d.cols < 1 || d.steps < 1) return LATENTMOE_ERR_INVALID_ARG;
   if (!(d.eps >= 1e-30f) || !isfinite(d.eps)) return LATENTMOE_ERR_INVALID_ARG;
-  if (d.rows > kMaxSide || d.cols > kMaxSide || d.batch > 65535 || d.steps > kMaxSteps)
+  if (d.rows > kMaxSide || d.cols > kMaxSide || d.batch > 65535 || d.steps > kNsMaxSteps)
     return LATENTMOE_ERR_UNSUPPORTED;
-  Step step[kMaxSteps];
+  lmoe::NsStep step[kNsMaxSteps];
+  memset(step, 0, sizeof(step));
   // bound on the spectral norm of X before the step: 1 after the division by
   // the Frobenius norm, then the largest value of |a s + b s^3 + c s^5| on
   // [0, bound], each a little more for rounding (the scales leave a factor of
   // 4; a wide margin here would leave the interval that the usual coefficients
   // keep to, and grow)
   double u = 1.001;
+  float scale0 = 1.0f;
   for (int i = 0; i < d.steps; ++i) {
-    Step& st = step[i];
-    st.a = d.coefs ? d.coefs[3 * i] : 3.4445f;
-    st.b = d.coefs ? d.coefs[3 * i + 1] : -4.7750f;
-    st.c = d.coefs ? d.coefs[3 * i + 2] : 2.0315f;
-    if (!isfinite(st.a) || !isfinite(st.b) || !isfinite(st.c)) return LATENTMOE_ERR_INVALID_ARG;
+    const float ca = d.coefs ? d.coefs[3 * i] : 3.4445f;
+    const float cb = d.coefs ? d.coefs[3 * i + 1] : -4.7750f;
+    const float cc = d.coefs ? d.coefs[3 * i + 2] : 2.0315f;
+    if (!isfinite(ca) || !isfinite(cb) || !isfinite(cc)) return LATENTMOE_ERR_INVALID_ARG;
     double next = 0.0, poly = 0.0;
     for (int j = 0; j <= 1024; ++j) {
       const double x = u * j / 1024.0, x2 = x * x;
-      const double p = st.b * x2 + st.c * x2 * x2;
+      const double p = cb * x2 + cc * x2 * x2;
       poly = fmax(poly, fabs(p));
-      next = fmax(next, fabs((st.a + p) * x));
+      next = fmax(next, fabs((ca + p) * x));
     }
-    st.sx = pow2_scale(u);
-    st.sa = pow2_scale(u * u);
-    st.sp = pow2_scale(poly);
+    const float sx = pow2_scale(u), sa = pow2_scale(u * u), sp = pow2_scale(poly);
+    lmoe::NsStep& f = step[i];
+    f.gram_diag = 1.0f / sx / sx;
+    f.gram_off = sa * f.gram_diag;
+    f.poly_b = cb * (sp / sa);
+    f.poly_c = cc * (sp / sa);
+    f.poly_acc = f.poly_c / sa;
+    f.diag_acc = cc / sa / sa;
+    f.b = cb;
+    f.c = cc;
+    f.s_p = sp;
+    f.d_x = 1.0f / sx;
+    if (i == 0) scale0 = sx;
+    else step[i - 1].d_x *= sx;  // the step before leaves X with this step's scale
     u = 1.002 * next;
     if (!(u < 1e6)) return LATENTMOE_ERR_INVALID_ARG;  // the coefficients diverge
     if (u < 1e-6) u = 1e-6;
   }
+  for (int i = 0; i < d.steps; ++i) {
+    step[i].a_x = (d.coefs ? d.coefs[3 * i] : 3.4445f) * step[i].d_x;
+    step[i].apply_acc = step[i].d_x / step[i].s_p;
+  }
   const long long B = d.batch, R = d.rows, C = d.cols;
   const long long side = R < C ? R : C;
   const long long ldx = (C + 7) / 8 * 8, lda = (side + 7) / 8 * 8;
-  // tile counts stay in int
-  const long long t128 = ((R + 127) / 128) * ((C + 127) / 128);
-  if (t128 * B > (1ll << 30)) return LATENTMOE_ERR_UNSUPPORTED;
+  // positions in the tile sequence stay in int
+  if ((2 * sym_tiles(side, 128) + tiles(R, C, 128)) * B * d.steps > (1ll << 30))
+    return LATENTMOE_ERR_UNSUPPORTED;
 
   latentmoe_muon* h = new (std::nothrow) latentmoe_muon();
   if (h == nullptr) return LATENTMOE_ERR_OUT_OF_MEMORY;
@@ -244,9 +221,24 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   h->tall = R > C;
   h->steps = static_cast<int>(d.steps);
   h->eps = d.eps;
-  memcpy(h->step, step, sizeof(step));
-  h->ldx = ldx;
-  h->lda = lda;
+  h->scale0 = scale0;
+  memset(&h->args, 0, sizeof(h->args));
+  NsArgs& a = h->args;
+  a.batch = static_cast<int>(B);
+  a.rows = static_cast<int>(R);
+  a.cols = static_cast<int>(C);
+  a.side = static_cast<int>(side);
+  a.tall = h->tall ? 1 : 0;
+  a.steps = h->steps;
+  a.k_gram = static_cast<int>(((R > C ? R : C) + lmoe::kNsBK - 1) / lmoe::kNsBK);
+  a.k_side = static_cast<int>((side + lmoe::kNsBK - 1) / lmoe::kNsBK);
+  a.ld_x = ldx;
+  a.ld_a = lda;
+  memcpy(a.step, step, sizeof(step));
+  // matrices in flight: what stays in L2
+  const long long bytes = 8 * R * ldx + 4 * side * lda;
+  long long group = kGroupBytes / bytes;
+  h->group = static_cast<int>(group < 1 ? 1 : group > B ? B : group);
   // blocks of the norm pass: 16 elements a thread or more, whole vectors
   const long long n = R * C;
   const long long unit = 8ll * lmoe::kNsNormThreads;
@@ -273,6 +265,9 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   const size_t o_x32 = take(xn * 4), o_x0 = take(xn * 2);
   const size_t o_x1 = h->steps > 1 ? take(xn * 2) : o_x0;
   const size_t o_gram = take(an * 2), o_poly = take(an * 2);
+  const size_t o_da = take(static_cast<size_t>(B) * lda * 4);
+  const size_t o_dp = take(static_cast<size_t>(B) * lda * 4);
+  const size_t o_done = take(static_cast<size_t>(B) * 3 * h->steps * 4), o_counter = take(16);
   const size_t o_partial = take(static_cast<size_t>(B) * h->chunks * 4), o_status = take(16);
   e = cudaMalloc(&h->ws, off);
   if (e != cudaSuccess) {
@@ -282,17 +277,27 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   }
   char* base = static_cast<char*>(h->ws);
   h->x32 = reinterpret_cast<float*>(base + o_x32);
-  h->x16[0] = reinterpret_cast<__half*>(base + o_x0);
-  h->x16[1] = reinterpret_cast<__half*>(base + o_x1);
-  h->gram = reinterpret_cast<__half*>(base + o_gram);
-  h->poly = reinterpret_cast<__half*>(base + o_poly);
+  h->x16 = reinterpret_cast<__half*>(base + o_x0);
+  void* x1 = base + o_x1;
+  void* gram = base + o_gram;
+  void* poly = base + o_poly;
+  a.diag_a = reinterpret_cast<float*>(base + o_da);
+  a.diag_p = reinterpret_cast<float*>(base + o_dp);
+  a.done = reinterpret_cast<int*>(base + o_done);
+  a.counter = reinterpret_cast<int*>(base + o_counter);
+  a.status = reinterpret_cast<unsigned*>(base + o_status);
   h->partial = reinterpret_cast<float*>(base + o_partial);
-  h->status = reinterpret_cast<unsigned*>(base + o_status);
-  e = cudaMemset(h->status, 0, 16);
-  if (e != cudaSuccess || !make_ns_map(&h->m_x[0], h->x16[0], B, R, C, ldx) ||
-      !make_ns_map(&h->m_x[1], h->x16[1], B, R, C, ldx) ||
-      !make_ns_map(&h->m_gram, h->gram, B, side, side, lda) ||
-      !make_ns_map(&h->m_poly, h->poly, B, side, side, lda)) {
+  e = cudaMemset(a.status, 0, 16);
+  lmoe::NsMaps& t = h->maps;
+  if (e != cudaSuccess || !make_ns_map(&t.x[0], h->x16, B, R, C, ldx, 64) ||
+      !make_ns_map(&t.x[1], x1, B, R, C, ldx, 64) ||
+      !make_ns_map(&t.gram, gram, B, side, side, lda, 64) ||
+      !make_ns_map(&t.poly, poly, B, side, side, lda, 64) ||
+      !make_ns_map(&t.chunk_h[0], h->x16, B, R, C, ldx, 32) ||
+      !make_ns_map(&t.chunk_h[1], x1, B, R, C, ldx, 32) ||
+      !make_ns_map(&t.chunk_x, h->x32, B, R, C, ldx, 32, true) ||
+      !make_ns_map(&t.chunk_gram, gram, B, side, side, lda, 32) ||
+      !make_ns_map(&t.chunk_poly, poly, B, side, side, lda, 32)) {
     cudaFree(h->ws);
     delete h;
     return LATENTMOE_ERR_CUDA;
@@ -352,8 +357,8 @@ int latentmoe_muon_get_status(latentmoe_muon_t h, uint32_t* device_status) {
   NS_CK(h, cudaSetDevice(h->device));
   NS_CK(h, cudaDeviceSynchronize());
   unsigned v = 0;
-  NS_CK(h, cudaMemcpy(&v, h->status, 4, cudaMemcpyDeviceToHost));
-  NS_CK(h, cudaMemset(h->status, 0, 4));
+  NS_CK(h, cudaMemcpy(&v, h->args.status, 4, cudaMemcpyDeviceToHost));
+  NS_CK(h, cudaMemset(h->args.status, 0, 4));
   *device_status = v;
   if (v & LATENTMOE_STATUS_TIMEOUT) return LATENTMOE_ERR_TIMEOUT;
   return v != 0 ? LATENTMOE_ERR_DEVICE_STATUS : LATENTMOE_OK;

@@ -4,7 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "ns_gemm.cuh"
+#include "ns_iterate.cuh"
 
 namespace lmoe {
 
@@ -23,17 +23,18 @@ struct NsUpdate {
 cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int chunks,
                            long long chunk, float* partial, cudaStream_t s);
 
-// X_0 = U / (|U|_F + eps): x32 [batch, rows, ld] and its fp16 copy times
-// `scale`; the padding columns are zero. U is formed as by launch_ns_norm from
-// the momentum that launch updated.
+// X_0 = U / (|U|_F + eps) times `scale` in fp32 and in fp16, [batch,
+// rows, ld]; the padding columns are zero. U is formed as by launch_ns_norm from
+// the momentum that launch updated. Sets the batch * phases counts at `done` and
+// the tile counter to zero.
 cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, long long cols,
                            long long ld, int chunks, const float* partial, float eps, float scale,
-                           float* x32, __half* x16, cudaStream_t s);
+                           float* x32, __half* x16, int* done, int phases, int* counter,
+                           cudaStream_t s);
 
-// One product. epi: NsEpi; tall: X has more rows than columns; pair: tiles of
-// 256 x 256 on SM pairs instead of 128 x 128 on single SMs. ma, mb: 3-D maps
-// (boxes of 64 columns x 64 rows x 1) of the two operands.
-cudaError_t launch_ns_gemm(int epi, bool tall, bool pair, const CUtensorMap& ma,
-                           const CUtensorMap& mb, const NsArgs& a, int sms, cudaStream_t s);
+// All steps in one launch. pair: tiles of 256 x 256 on SM pairs instead of
+// 128 x 128 on single SMs.
+cudaError_t launch_ns_iterate(bool pair, const NsMaps& m, const NsArgs& a, int sms,
+                              cudaStream_t s);
 
 }  // namespace lmoe

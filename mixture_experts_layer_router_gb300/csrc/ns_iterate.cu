@@ -1,0 +1,53 @@
+// Launcher of the Newton-Schulz iteration.
+#include "kernels.h"
+#include "ns.h"
+
+namespace lmoe {
+
+template <bool PAIR>
+static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cudaStream_t s) {
+  static int units_of[kMaxDevices] = {};
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  int& most = units_of[dev];
+  if (most == 0) {
+    cudaError_t e = cudaFuncSetAttribute(
+        ns_iterate_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes);
+    if (e != cudaSuccess) return e;
+    int n = sms;
+    if (PAIR) {
+      // pairs that can be resident at once
+      cudaLaunchConfig_t cfg;
+      memset(&cfg, 0, sizeof(cfg));
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+      cfg.blockDim = dim3(kNsThreads, 1, 1);
+      cfg.dynamicSmemBytes = kNsSmemBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n, ns_iterate_kernel<PAIR>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n > sms / 2) n = sms / 2;
+    }
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    most = n;
+  }
+  // no more units than the widest phase of all matrices in flight has tiles
+  const long long wide = static_cast<long long>(a.sym_tiles > a.apply_tiles ? a.sym_tiles
+                                                                            : a.apply_tiles) *
+                         a.batch;
+  const int units = static_cast<int>(wide < most ? wide : most);
+  return launch_kernel(ns_iterate_kernel<PAIR>, dim3(static_cast<unsigned>(PAIR ? 2 * units : units)),
+                       dim3(kNsThreads), kNsSmemBytes, s, PAIR ? 2 : 1, false, m, a);
+}
+
+cudaError_t launch_ns_iterate(bool pair, const NsMaps& m, const NsArgs& a, int sms,
+                              cudaStream_t s) {
+  return pair ? launch_ns_impl<true>(m, a, sms, s) : launch_ns_impl<false>(m, a, sms, s);
+}
+
+}  // namespace lmoe

@@ -8,7 +8,7 @@
 // scaled: the first reads g (and reads and writes m) and leaves one partial
 // sum of squares per block, the second adds the partials in a fixed order in
 // every block (the result does not depend on scheduling), forms U again and
-// writes X_0 in fp32 and in scaled fp16. Both are bound by memory traffic.
+// writes X_0 in fp32 and fp16. Both are bound by memory traffic.
 // U is formed with separately rounded products and sums, so that the momentum
 // equals m.mul_(mu).add_(g) bit for bit. The sum of squares is held in fp32:
 // a matrix whose norm reaches 1.8e19 has an infinite sum, and X_0 = 0.
@@ -116,11 +116,15 @@ template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kNsNormThreads)
     ns_init_kernel(const void* g, const float* mom, float mu,
                    int nesterov, long long rows, long long cols, long long ld, int chunks,
-                   const float* partial, float eps, float scale,
-                   float* x32, __half* x16) {
+                   const float* partial, float eps, float scale, float* x32, __half* x16,
+                   int* done, int phases, int* counter) {
   pdl_wait();
   pdl_launch_dependents();
   const long long b = blockIdx.y;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < phases; i += kNsNormThreads) done[b * phases + i] = 0;
+    if (b == 0 && threadIdx.x == 0) *counter = 0;
+  }
   float s = 0.0f;
   for (int c = threadIdx.x; c < chunks; c += kNsNormThreads) s += partial[b * chunks + c];
   const float inv = 1.0f / (sqrtf(block_sum(s)) + eps);
@@ -156,12 +160,12 @@ __global__ void __launch_bounds__(kNsNormThreads)
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= inv;
     const long long to = (b * rows + r) * ld + c;
-    *reinterpret_cast<float4*>(x32 + to) = make_float4(v[0], v[1], v[2], v[3]);
-    __half2 h01 = __floats2half2_rn(v[0] * scale, v[1] * scale);
-    __half2 h23 = __floats2half2_rn(v[2] * scale, v[3] * scale);
+    const float4 x = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+    *reinterpret_cast<float4*>(x32 + to) = x;
+    const __half2 h01 = __floats2half2_rn(x.x, x.y), h23 = __floats2half2_rn(x.z, x.w);
     uint2 w;
-    w.x = *reinterpret_cast<uint32_t*>(&h01);
-    w.y = *reinterpret_cast<uint32_t*>(&h23);
+    w.x = *reinterpret_cast<const uint32_t*>(&h01);
+    w.y = *reinterpret_cast<const uint32_t*>(&h23);
     *reinterpret_cast<uint2*>(x16 + to) = w;
   }
 }
@@ -186,7 +190,8 @@ cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int 
 
 cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, long long cols,
                            long long ld, int chunks, const float* partial, float eps, float scale,
-                           float* x32, __half* x16, cudaStream_t s) {
+                           float* x32, __half* x16, int* done, int phases, int* counter,
+                           cudaStream_t s) {
   long long blocks = (rows * (ld / 4) + 4 * kNsNormThreads - 1) / (4 * kNsNormThreads);
   if (blocks > 4096) blocks = 4096;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(batch));
@@ -196,13 +201,17 @@ cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, l
   const bool vec = cols % 4 == 0;
   if (u.g_f32)
     return vec ? launch_kernel(ns_init_kernel<true, true>, grid, block, 0, s, 1, false, u.g, mom,
-                               u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16)
+                               u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16,
+                               done, phases, counter)
                : launch_kernel(ns_init_kernel<true, false>, grid, block, 0, s, 1, false, u.g, mom,
-                               u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16);
+                               u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16,
+                               done, phases, counter);
   return vec ? launch_kernel(ns_init_kernel<false, true>, grid, block, 0, s, 1, false, u.g, mom,
-                             u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16)
+                             u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16,
+                               done, phases, counter)
              : launch_kernel(ns_init_kernel<false, false>, grid, block, 0, s, 1, false, u.g, mom,
-                             u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16);
+                             u.mu, nes, rows, cols, ld, chunks, partial, eps, scale, x32, x16,
+                               done, phases, counter);
 }
 
 }  // namespace lmoe
