@@ -188,10 +188,24 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None  # () -> handle of the current stream
+
+
 def _stream(stream) -> Optional[int]:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        # without building a Stream object (3 us, a fifth of a small call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or dev is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            torch.cuda.current_stream()  # CUDA is initialised from here on
+            _raw_stream = lambda: raw(dev())  # noqa: E731
+    return _raw_stream()
 
 
 class LatentMoE:
@@ -322,17 +336,16 @@ class LatentMoE:
     def _rows(self, t, name: str, T: int):
         """Row stride of a [T, E] fp32 tensor whose columns are contiguous."""
         import torch
-        _need(t.is_cuda and t.dtype == torch.float32 and
-              tuple(t.shape) == (T, self.dims.num_experts) and
-              (t.stride(1) == 1 or t.shape[1] == 1),
-              f"{name} must be a float32 CUDA tensor [{T}, {self.dims.num_experts}] with "
-              "contiguous rows")
-        return t.stride(0) if T > 1 else self.dims.num_experts
+        E = self.dims.num_experts
+        if not (t.dtype is torch.float32 and t.is_cuda and t.shape == (T, E) and
+                (E == 1 or t.stride(1) == 1)):
+            raise ValueError(f"{name} must be a float32 CUDA tensor [{T}, {E}] with contiguous "
+                             "rows")
+        return t.stride(0) if T > 1 else E
 
     def _per_slot(self, t, name: str, T: int, dtype) -> None:
-        _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == (T, self.k) and
-              t.is_contiguous(),
-              f"{name} must be a contiguous {dtype} CUDA tensor [{T}, {self.k}]")
+        if not (t.dtype is dtype and t.is_cuda and t.shape == (T, self.k) and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{T}, {self.k}]")
 
     def _sequences(self, T: int, seq_len: int) -> int:
         L = seq_len or T
@@ -352,26 +365,29 @@ class LatentMoE:
         """The router's balance loss of logits [T, E] fp32 and choices idx
         [T, k] int32: {"loss": [total, balance, z], "counts" [S, E] int32,
         "prob_sum" [S, E], "z_sum" [S], "tokens" [S] int32} over S = T /
-        seq_len sequences (0: one)."""
+        seq_len sequences (0: one). The five are views of one allocation."""
         import torch
         T, E = logits.shape[0], self.dims.num_experts
         ld = self._rows(logits, "logits", T)
         self._per_slot(idx, "idx", T, torch.int32)
         S = self._sequences(T, seq_len)
-        # one allocation: counts, tokens, prob_sum, z_sum, loss
-        ints = torch.empty((S * (E + 1),), dtype=torch.int32, device=logits.device)
-        flts = torch.empty((S * (E + 1) + 3,), dtype=torch.float32, device=logits.device)
-        ip, fp = ints.data_ptr(), flts.data_ptr()
-        n = 4 * S * E
-        st = latentmoe_balance_stats(ip, fp, fp + n, ip + n)
+        n = S * E
+        # counts, tokens, prob_sum, z_sum, loss
+        flts = torch.empty((2 * (n + S) + 3,), dtype=torch.float32, device=logits.device)
+        p = flts.data_ptr()
+        at = (0, n, n + S, 2 * n + S, 2 * (n + S))
+        st = latentmoe_balance_stats(p, p + 4 * at[2], p + 4 * at[3], p + 4 * at[1])
         check(load().latentmoe_balance_loss(
             self.handle, logits.data_ptr(), ld, idx.data_ptr(), self._valid(valid, T), T, seq_len,
-            balance_coef, z_coef, ctypes.byref(st), fp + n + 4 * S, _stream(stream)),
+            balance_coef, z_coef, ctypes.byref(st), p + 4 * at[4], _stream(stream)),
             "latentmoe_balance_loss", self.handle)
-        counts, tokens = ints.split((S * E, S))
-        prob, z, loss = flts.split((S * E, S, 3))
-        return {"loss": loss, "counts": counts.view(S, E), "prob_sum": prob.view(S, E),
-                "z_sum": z, "tokens": tokens}
+        ints = flts.view(torch.int32)
+        rows, one = (S, E), (E, 1)
+        return {"loss": flts.as_strided((3,), (1,), at[4]),
+                "counts": ints.as_strided(rows, one, 0),
+                "prob_sum": flts.as_strided(rows, one, at[2]),
+                "z_sum": flts.as_strided((S,), (1,), at[3]),
+                "tokens": ints.as_strided((S,), (1,), at[1])}
 
     def balance_loss_from_stats(self, stats, balance_coef: float = 1.0, z_coef: float = 0.0,
                                 stream=None):
@@ -406,8 +422,9 @@ class LatentMoE:
         if d_gates is not None:
             self._per_slot(d_gates, "d_gates", T, torch.float32)
         for t, name, shape in ((counts, "counts", (S, E)), (tokens, "tokens", (S,))):
-            _need(t.is_cuda and t.dtype == torch.int32 and tuple(t.shape) == shape and
-                  t.is_contiguous(), f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
+            if not (t.dtype is torch.int32 and t.is_cuda and t.shape == shape and
+                    t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
         if d_loss is not None:
             _need(d_loss.is_cuda and d_loss.dtype == torch.float32 and d_loss.numel() == 1,
                   "d_loss must be one float32 on the GPU")

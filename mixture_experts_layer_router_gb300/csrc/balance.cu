@@ -31,10 +31,10 @@ namespace lmoe {
 
 namespace {
 
-constexpr int kBalThreads = 1024;
+constexpr int kBalThreads = 512;  // E <= 512: a thread an expert in the tail
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalGroup = 16;  // CTAs whose partial sums one CTA adds
-constexpr int kBackThreads = 512;
+constexpr int kBackThreads = 128;
 
 // How a row of E logits lies in a warp's registers.
 template <int LANES_, int NV_, bool VEC_>
@@ -47,6 +47,7 @@ struct Row {
   static constexpr int U = NV >= 3 ? 1 : 4 / NV;  // of those in flight
   static constexpr int BATCH = ROWS * U;
   static constexpr int WIDTH = LANES * N;       // columns covered, >= E
+  static constexpr int J = (16 + LANES - 1) / LANES;  // choices a lane (k <= 16)
   // column of element i of lane q
   __device__ static __forceinline__ int col(int q, int i) {
     return VEC ? 4 * (q + LANES * (i >> 2)) + (i & 3) : q + LANES * i;
@@ -71,34 +72,93 @@ struct Row {
       }
     }
   }
-  __device__ static __forceinline__ float sum(float v) {
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  }
-  __device__ static __forceinline__ float max(float v) {
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-  }
 };
 
-// x <- exp(x - max) over the row; returns the sum, and the max in m. A row of
-// -inf alone gives sum 0 (and max 0); a NaN makes the sum NaN.
-template <class R>
-__device__ __forceinline__ float row_exp(float (&x)[R::N], float& m) {
-  m = x[0];
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// V values (1, 2 or 4) reduced over the LANES lanes of a row at once; every lane
+// gets all results. Halves (quarters) of the lanes first take over one value
+// each, so V = 4 takes 2 + 1 + (log2 LANES - 2) + 4 shuffles instead of 4 log2
+// LANES. A fixed order.
+template <int LANES, int V, class Op>
+__device__ __forceinline__ void reduce_row(float (&v)[V], Op op) {
+  static_assert(V == 1 || V == 2 || V == 4, "values");
+  static_assert(LANES >= V, "lanes");
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  if constexpr (V == 1) {
 #pragma unroll
-  for (int i = 1; i < R::N; ++i) m = fmaxf(m, x[i]);
-  m = R::max(m);
-  if (m == -INFINITY) m = 0.0f;
-  float s = 0.0f;
+    for (int o = LANES / 2; o > 0; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(kAll, v[0], o));
+  } else if constexpr (V == 2) {
+    const bool up = (lane & (LANES / 2)) != 0;
+    float w = op(up ? v[1] : v[0], __shfl_xor_sync(kAll, up ? v[0] : v[1], LANES / 2));
 #pragma unroll
-  for (int i = 0; i < R::N; ++i) {
-    x[i] = __expf(x[i] - m);
-    s += x[i];
+    for (int o = LANES / 4; o > 0; o >>= 1) w = op(w, __shfl_xor_sync(kAll, w, o));
+    v[0] = __shfl_sync(kAll, w, 0, LANES);
+    v[1] = __shfl_sync(kAll, w, LANES / 2, LANES);
+  } else {
+    const bool up = (lane & (LANES / 2)) != 0;
+    const float a = op(up ? v[2] : v[0], __shfl_xor_sync(kAll, up ? v[0] : v[2], LANES / 2));
+    const float b = op(up ? v[3] : v[1], __shfl_xor_sync(kAll, up ? v[1] : v[3], LANES / 2));
+    const bool up2 = (lane & (LANES / 4)) != 0;
+    float w = op(up2 ? b : a, __shfl_xor_sync(kAll, up2 ? a : b, LANES / 4));
+#pragma unroll
+    for (int o = LANES / 8; o > 0; o >>= 1) w = op(w, __shfl_xor_sync(kAll, w, o));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kAll, w, i * (LANES / 4), LANES);
   }
-  return R::sum(s);
+}
+
+// Exponentials as powers of two: exp(x - max) = 2^(c x - top) with c = log2 e and
+// top = c max rounded once, which is one fused multiply-add and one special
+// function. The rounding of top is common to a row: it cancels in p, and
+// lse = (top + log2(sum)) / c takes the same top. The special functions are the
+// hardware's (2 ulp): errors of p and lse stay below 4e-6.
+constexpr float kLog2E = 1.44269504f;
+constexpr float kLn2 = 0.693147181f;
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float recip(float x) { return __fdividef(1.0f, x); }
+
+// The tops of a batch's rows (0 for a row of -inf alone).
+template <class R>
+__device__ __forceinline__ void row_tops(const float (&x)[R::U][R::N], float (&top)[R::U]) {
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) {
+    float m = x[u][0];
+#pragma unroll
+    for (int i = 1; i < R::N; ++i) m = fmaxf(m, x[u][i]);
+    top[u] = m;
+  }
+  reduce_row<R::LANES>(top, Max());
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) top[u] = top[u] == -INFINITY ? 0.0f : top[u] * kLog2E;
+}
+// x <- 2^(c x - top); the lane's part of the sum. A row of -inf alone sums to 0,
+// a NaN makes its row's sum NaN.
+template <class R>
+__device__ __forceinline__ float row_exp(float (&x)[R::N], float top) {
+  float s = 0.0f, s2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R::N; i += 2) {
+    x[i] = pow2(fmaf(x[i], kLog2E, -top));
+    x[i + 1] = pow2(fmaf(x[i + 1], kLog2E, -top));
+    s += x[i];
+    s2 += x[i + 1];
+  }
+  return s + s2;
+}
+// lse of a row from its top and sum (>= about 1).
+__device__ __forceinline__ float row_lse(float top, float sum) {
+  return (top + __log2f(sum)) * kLn2;
 }
 
 // Fixed-order sum over the block; every thread gets it. `buf`: kBalWarps floats.
@@ -109,7 +169,7 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
   __syncthreads();
   if (lane == 0) buf[warp] = v;
   __syncthreads();
-  float t = buf[lane];  // kBalWarps == 32
+  float t = lane < kBalWarps ? buf[lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
@@ -140,6 +200,32 @@ __device__ __forceinline__ void store_loss(float* loss, float balance, float z, 
 }
 
 }  // namespace
+
+// What the loss reads for one batch of rows.
+template <class R>
+struct LossRows {
+  float x[R::U][R::N];
+  int id[R::U][R::J];
+  bool in[R::U];
+  int valid[R::U];  // compared when it is used: a comparison here would wait for the load
+  __device__ __forceinline__ void load(const BalanceArgs& a, long long t0, int base, int r1, int q,
+                                       int sub) {
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int r = base + u * R::ROWS + sub;
+      const long long t = t0 + r;
+      in[u] = r < r1;
+      // a row past the part is read as the batch's first row (in range) and dropped
+      R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, a.E, x[u]);
+#pragma unroll
+      for (int j = 0; j < R::J; ++j) {
+        const int c = q + R::LANES * j;
+        id[u][j] = in[u] && c < a.k ? a.idx[t * a.k + c] : -1;
+      }
+      valid[u] = in[u] && a.valid != nullptr ? a.valid[t] : 1;
+    }
+  }
+};
 
 // Unit u: part u % parts of sequence u / parts. With one part a sequence the
 // CTA has the sequence's sums itself; otherwise the last CTA of each group of
@@ -172,41 +258,54 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     float zsum = 0.0f;
     int ntok = 0;
     bool bad = false;
-    for (int base = r0 + warp * R::BATCH; base < r1; base += kBalWarps * R::BATCH) {
-      float x[R::U][R::N];
-      bool in[R::U];
+    constexpr int kStride = kBalWarps * R::BATCH;
+    int base = r0 + warp * R::BATCH;
+    auto add = [&](LossRows<R>& cur) {
+      float top[R::U], sums[R::U];
+      row_tops<R>(cur.x, top);
+#pragma unroll
+      for (int u = 0; u < R::U; ++u) sums[u] = row_exp<R>(cur.x[u], top[u]);
+      reduce_row<R::LANES>(sums, Add());
 #pragma unroll
       for (int u = 0; u < R::U; ++u) {
-        const int r = base + u * R::ROWS + sub;
-        const long long t = t0 + r;
-        in[u] = r < r1;
-        // a row past the part is read as the batch's first row (in range) and dropped
-        R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, E, x[u]);
-        if (in[u] && a.valid != nullptr) in[u] = a.valid[t] != 0;
-      }
-#pragma unroll
-      for (int u = 0; u < R::U; ++u) {
-        const long long t = t0 + base + u * R::ROWS + sub;
-        float m;
-        const float sum = row_exp<R>(x[u], m);
-        const bool ok = in[u] && !(sum == 0.0f);
-        const float inv = 1.0f / sum;
+        const float sum = sums[u];
+        const bool ok = cur.in[u] && cur.valid[u] != 0 && !(sum == 0.0f);
+        const float inv = recip(sum);
         if (ok) {
 #pragma unroll
-          for (int i = 0; i < R::N; ++i) acc[i] = fmaf(x[u][i], inv, acc[i]);
+          for (int i = 0; i < R::N; ++i) acc[i] = fmaf(cur.x[u][i], inv, acc[i]);
           if (q == 0) {
-            const float lse = m + logf(sum);
+            const float lse = row_lse(top[u], sum);
             zsum = fmaf(lse, lse, zsum);
             ntok += 1;
           }
-          for (int j = q; j < k; j += R::LANES) {
-            const int id = a.idx[t * k + j];
-            if (static_cast<unsigned>(id) < static_cast<unsigned>(E))
-              atomicAdd(&hist[id], 1);
-            else
-              bad = true;
+#pragma unroll
+          for (int j = 0; j < R::J; ++j) {
+            if (q + R::LANES * j < k) {
+              const int id = cur.id[u][j];
+              if (static_cast<unsigned>(id) < static_cast<unsigned>(E))
+                atomicAdd(&hist[id], 1);
+              else
+                bad = true;
+            }
           }
         }
+      }
+    };
+    // two sets of registers in turn: the next batch's rows are on their way
+    // while this one's are summed
+    if (base < r1) {
+      LossRows<R> even, odd;
+      even.load(a, t0, base, r1, q, sub);
+      while (true) {
+        base += kStride;
+        if (base < r1) odd.load(a, t0, base, r1, q, sub);
+        add(even);
+        if (base >= r1) break;
+        base += kStride;
+        if (base < r1) even.load(a, t0, base, r1, q, sub);
+        add(odd);
+        if (base >= r1) break;
       }
     }
     if (bad) atomicOr(a.status, kStatusBadExpert);
@@ -232,12 +331,12 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       warp_n[warp] = ntok;
     }
     __syncthreads();
-    // thread e owns expert e from here on (E <= 512 < kBalThreads)
+    // thread e owns expert e from here on (E <= kBalThreads)
     const int e = threadIdx.x;
     float prob = 0.0f, z = 0.0f;
     int count = 0, n = 0;
     if (e < E) {
-#pragma unroll 8
+#pragma unroll
       for (int v = 0; v < kBalWarps; ++v) prob += red[v * E + e];
       count = hist[e];
     }
@@ -266,17 +365,29 @@ __global__ void __launch_bounds__(kBalThreads, 1)
           }
           mine = arrive_last(ticket, static_cast<unsigned>(rows), &flag);
           if (mine) {
-            prob = z = 0.0f;
-            count = n = 0;
-#pragma unroll 4
-            for (int v = 0; v < rows; ++v) {
+            prob = 0.0f;
+            count = 0;
+            // the loads of a sum in flight at once
+            float pv[kBalGroup];
+            int cv[kBalGroup];
+#pragma unroll
+            for (int v = 0; v < kBalGroup; ++v) {
               const long long from = first + v;
-              if (e < E) {
-                prob += __ldcg(w.prob + from * E + e);
-                count += __ldcg(w.count + from * E + e);
-              }
-              z += __ldcg(w.z + from);
-              n += __ldcg(w.tokens + from);
+              const bool has = v < rows && e < E;
+              pv[v] = has ? __ldcg(w.prob + from * E + e) : 0.0f;
+              cv[v] = has ? __ldcg(w.count + from * E + e) : 0;
+            }
+            z = lane < rows ? __ldcg(w.z + first + lane) : 0.0f;
+            n = lane < rows ? __ldcg(w.tokens + first + lane) : 0;
+#pragma unroll
+            for (int v = 0; v < kBalGroup; ++v) {
+              prob += pv[v];
+              count += cv[v];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              z += __shfl_xor_sync(0xffffffffu, z, o);
+              n += __shfl_xor_sync(0xffffffffu, n, o);
             }
           }
         }
@@ -349,6 +460,53 @@ __global__ void __launch_bounds__(kBalThreads)
   if (threadIdx.x == 0) store_loss(loss, bs, zs, bc, zc);
 }
 
+// What the backward reads for one batch of rows: the logits and, for the
+// gates' part, the lane's choices, their gradients and their logits.
+template <class R, bool GATES>
+struct BackRows {
+  float x[R::U][R::N];
+  bool in[R::U];
+  int valid[R::U];
+  int id[GATES ? R::U : 1][R::J];
+  float dg[GATES ? R::U : 1][R::J], xi[GATES ? R::U : 1][R::J];
+  __device__ __forceinline__ void load(const RouterBackwardArgs& a, long long t0, int base, int r1,
+                                       int q, int sub) {
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int r = base + u * R::ROWS + sub;
+      const long long t = t0 + r;
+      in[u] = r < r1;
+      if constexpr (GATES) {
+#pragma unroll
+        for (int j = 0; j < R::J; ++j) {
+          const int c = q + R::LANES * j;
+          const bool has = in[u] && c < a.k;
+          id[u][j] = has ? a.idx[t * a.k + c] : -1;
+          dg[u][j] = has ? a.d_gates[t * a.k + c] : 0.0f;
+        }
+      }
+      R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, a.E, x[u]);
+      valid[u] = in[u] && a.valid != nullptr ? a.valid[t] : 1;
+    }
+  }
+  // after load: the choices' logits (ids outside [0, E): none)
+  __device__ __forceinline__ void gather(const RouterBackwardArgs& a, long long t0, int base,
+                                         int sub) {
+    if constexpr (GATES) {
+#pragma unroll
+      for (int u = 0; u < R::U; ++u) {
+        const float* row = a.logits + (t0 + base + u * R::ROWS + sub) * a.ld;
+#pragma unroll
+        for (int j = 0; j < R::J; ++j) {
+          const bool has = static_cast<unsigned>(id[u][j]) < static_cast<unsigned>(a.E);
+          if (!has) id[u][j] = -1;
+          xi[u][j] = has ? row[id[u][j]] : -INFINITY;
+        }
+      }
+    }
+  }
+};
+
 // d_logits. The gates' part, with D = sum_j g_j dg_j over the token's choices:
 //   g_j = p[idx_j]:            sum_{j: idx_j = e} g_j dg_j  -  p_e D
 //   g_j = p[idx_j] / sum_i p[idx_i], i.e. a softmax over the chosen logits
@@ -386,82 +544,95 @@ __global__ void __launch_bounds__(kBackThreads)
     const int c = R::col(q, i);
     wt[i] = c < E ? wc * static_cast<float>(a.counts[static_cast<long long>(s) * E + c]) : 0.0f;
   }
-  for (int base = r0 + warp * R::BATCH; base < r1; base += (kBackThreads / 32) * R::BATCH) {
-    float x[R::U][R::N];
-    bool in[R::U], counted[R::U];
-#pragma unroll
-    for (int u = 0; u < R::U; ++u) {
-      const int r = base + u * R::ROWS + sub;
-      const long long t = t0 + r;
-      in[u] = r < r1;
-      counted[u] = in[u];
-      R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, E, x[u]);
-      if (in[u] && a.valid != nullptr) counted[u] = a.valid[t] != 0;
+  constexpr int kStride = (kBackThreads / 32) * R::BATCH;
+  // with one choice a lane there are registers for a second batch: its rows are
+  // on their way while the first one's are worked on
+  constexpr bool kAhead = R::J == 1;
+  BackRows<R, GATES> cur;
+  int base = r0 + warp * R::BATCH;
+  if (kAhead && base < r1) cur.load(a, t0, base, r1, q, sub);
+  for (; base < r1; base += kStride) {
+    BackRows<R, GATES> next;
+    if constexpr (kAhead) {
+      if (base + kStride < r1) next.load(a, t0, base + kStride, r1, q, sub);
+    } else {
+      cur.load(a, t0, base, r1, q, sub);
     }
+    cur.gather(a, t0, base, sub);
+    float top[R::U];
+    row_tops<R>(cur.x, top);
 #pragma unroll
     for (int u = 0; u < R::U; ++u) {
       const long long t = t0 + base + u * R::ROWS + sub;
-      float m;
-      const float sum = row_exp<R>(x[u], m);
-      const bool empty = sum == 0.0f;
-      const float inv = empty ? 0.0f : 1.0f / sum;
-      float dot = 0.0f;
+      // the row's sum and sum of w e; with gates also the sums of the choices'
+      // e and of e dg
+      float v[GATES ? 4 : 2];
+      v[0] = row_exp<R>(cur.x[u], top[u]);
+      v[1] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) dot = fmaf(x[u][i], wt[i], dot);
-      dot = R::sum(dot) * inv;
+      for (int i = 0; i < R::N; ++i) v[1] = fmaf(cur.x[u][i], wt[i], v[1]);
+      float g[R::J];
+      if constexpr (GATES) {
+        v[2] = v[3] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < R::J; ++j) {
+          g[j] = cur.id[u][j] >= 0 ? pow2(fmaf(cur.xi[u][j], kLog2E, -top[u])) : 0.0f;
+          v[2] += g[j];
+          v[3] = fmaf(g[j], cur.dg[u][j], v[3]);
+        }
+      }
+      reduce_row<R::LANES>(v, Add());
+      const float sum = v[0];
+      const bool empty = sum == 0.0f;
+      const float inv = empty ? 0.0f : recip(sum);
       // p_e (wt_e + shift)
-      const bool on = counted[u] && !empty;
-      float shift = on ? fmaf(zq, m + logf(sum), -dot) : 0.0f;
+      const bool on = cur.in[u] && cur.valid[u] != 0 && !empty;
+      float shift = on ? fmaf(zq, row_lse(top[u], sum), -v[1] * inv) : 0.0f;
       float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
       if constexpr (GATES) {
-        const float* row = a.logits + t * a.ld;
-        // the choices' logits; D; for the renormalised form their own max and sum
-        float best = -INFINITY;
+        float gs = v[2], gd = v[3], ginv = inv;
         if (a.renorm) {
-          for (int j = q; j < k; j += R::LANES) {
-            const int id = in[u] ? a.idx[t * k + j] : -1;
-            if (static_cast<unsigned>(id) < static_cast<unsigned>(E)) best = fmaxf(best, row[id]);
+          // choices so far below the row's maximum that they (nearly) underflow,
+          // as replayed ones may be: once more from their own maximum
+          if (__any_sync(0xffffffffu, cur.in[u] && gs < 1e-30f)) {
+            float m[1] = {cur.xi[u][0]};
+#pragma unroll
+            for (int j = 1; j < R::J; ++j) m[0] = fmaxf(m[0], cur.xi[u][j]);
+            reduce_row<R::LANES>(m, Max());
+            const float own = m[0] == -INFINITY ? 0.0f : m[0] * kLog2E;
+            float w[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < R::J; ++j) {
+              g[j] = cur.id[u][j] >= 0 ? pow2(fmaf(cur.xi[u][j], kLog2E, -own)) : 0.0f;
+              w[0] += g[j];
+              w[1] = fmaf(g[j], cur.dg[u][j], w[1]);
+            }
+            reduce_row<R::LANES>(w, Add());
+            gs = w[0];
+            gd = w[1];
           }
-          best = R::max(best);
-          if (best == -INFINITY) best = 0.0f;
+          ginv = gs == 0.0f ? 0.0f : recip(gs);
         }
-        float gs = 0.0f, gd = 0.0f;
-        for (int j = q; j < k; j += R::LANES) {
-          const int id = in[u] ? a.idx[t * k + j] : -1;
-          if (static_cast<unsigned>(id) < static_cast<unsigned>(E)) {
-            const float g = a.renorm ? __expf(row[id] - best) : __expf(row[id] - m) * inv;
-            gs += g;
-            gd = fmaf(g, a.d_gates[t * k + j], gd);
-          }
-        }
-        gd = R::sum(gd);
-        float ginv = 1.0f;
-        if (a.renorm) {
-          gs = R::sum(gs);
-          ginv = gs == 0.0f ? 0.0f : 1.0f / gs;
-          gd *= ginv;
-        } else {
+        gd *= ginv;
+        if (!a.renorm) {
           shift -= gd;
+          gd = 0.0f;
         }
-        // whole warp: k / LANES rounds, one choice a lane
-        for (int j0 = 0; j0 < k; j0 += R::LANES) {
-          const int j = j0 + q;
-          const int id = in[u] && j < k ? a.idx[t * k + j] : -1;
-          const bool has = static_cast<unsigned>(id) < static_cast<unsigned>(E);
-          float v = 0.0f;
-          if (has) {
-            const float dg = a.d_gates[t * k + j];
-            v = a.renorm ? __expf(row[id] - best) * ginv * (dg - gd)
-                         : __expf(row[id] - m) * inv * dg;
-          }
+        // whole warp: one choice a lane in each round
+#pragma unroll
+        for (int j = 0; j < R::J; ++j) {
+          if (R::LANES * j >= k) break;
+          const bool has = cur.id[u][j] >= 0;
+          const float v = g[j] * ginv * (cur.dg[u][j] - gd);
           // a token's choices differ as a rule; given choices may repeat, and
           // then their terms are added in the order of the choices
-          const unsigned same = __match_any_sync(0xffffffffu, has ? sub * 1024 + id : -1 - lane);
+          const unsigned same =
+              __match_any_sync(0xffffffffu, has ? sub * 1024 + cur.id[u][j] : -1 - lane);
           if (__all_sync(0xffffffffu, __popc(same) == 1)) {
-            if (has) mine[id] += v;
+            if (has) mine[cur.id[u][j]] += v;
           } else {
             for (int o = 0; o < R::LANES; ++o) {
-              if (has && q == o) mine[id] += v;
+              if (has && q == o) mine[cur.id[u][j]] += v;
               __syncwarp();
             }
           }
@@ -473,19 +644,32 @@ __global__ void __launch_bounds__(kBackThreads)
       float d[R::N];
 #pragma unroll
       for (int i = 0; i < R::N; ++i) {
-        const float v = (x[u][i] * inv) * (on ? wt[i] + shift : shift);
+        const float v = (cur.x[u][i] * inv) * (on ? wt[i] + shift : shift);
         d[i] = GATES || on ? v : 0.0f;
       }
       if constexpr (GATES) {
+        if constexpr (R::VEC) {
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) {
-          const int c = R::col(q, i);
-          d[i] += mine[c];
-          mine[c] = 0.0f;
+          for (int v = 0; v < R::NV; ++v) {
+            float4* at = reinterpret_cast<float4*>(mine + 4 * (q + R::LANES * v));
+            const float4 f = *at;
+            *at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            d[4 * v] += f.x;
+            d[4 * v + 1] += f.y;
+            d[4 * v + 2] += f.z;
+            d[4 * v + 3] += f.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < R::N; ++i) {
+            const int c = R::col(q, i);
+            d[i] += mine[c];
+            mine[c] = 0.0f;
+          }
         }
         __syncwarp();
       }
-      if (in[u]) {
+      if (cur.in[u]) {
         float* out = a.d_logits + t * a.ldd;
         if constexpr (R::VEC) {
 #pragma unroll
@@ -504,6 +688,7 @@ __global__ void __launch_bounds__(kBackThreads)
         }
       }
     }
+    if constexpr (kAhead) cur = next;
   }
 }
 
@@ -528,6 +713,7 @@ cudaError_t loss_impl(const BalanceArgs& a, const BalanceScratch& w, cudaStream_
   int parts = w.units / a.seqs;
   const int most = div_up(a.seq_len, kBalWarps * R::BATCH);
   if (parts > most) parts = most;
+  if (parts > kBalGroup * kBalGroup) parts = kBalGroup * kBalGroup;  // two levels of sums
   if (parts < 1) parts = 1;
   const int part_rows = div_up(a.seq_len, parts);
   parts = div_up(a.seq_len, part_rows);
@@ -541,12 +727,22 @@ template <class R, bool GATES>
 cudaError_t backward_impl(const RouterBackwardArgs& a, int sms, cudaStream_t s) {
   constexpr int warps = kBackThreads / 32;
   const int smem = GATES ? warps * R::U * R::ROWS * R::WIDTH * 4 : 0;
-  // a CTA's rows: two batches a warp, or more once every SM has eight CTAs
-  const long long T = static_cast<long long>(a.seqs) * a.seq_len;
-  long long rows = 2ll * warps * R::BATCH;
-  const long long fill = (T + 8ll * sms - 1) / (8ll * sms);
-  if (rows < fill) rows = fill;
-  int parts = div_up(a.seq_len, rows);
+  static int resident_of[kMaxDevices] = {};
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (resident_of[dev] == 0) {
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &n, router_backward_kernel<R, GATES>, kBackThreads, smem);
+    if (e != cudaSuccess) return e;
+    resident_of[dev] = n > 0 ? n : 1;
+  }
+  // parts of a sequence: a batch of rows for every warp, but no more CTAs in
+  // all than the SMs hold at once
+  const int slots = resident_of[dev] * sms;
+  int parts = div_up(a.seq_len, warps * R::BATCH);
+  if (parts > slots / a.seqs) parts = slots / a.seqs;
+  if (parts < 1) parts = 1;
   const int part_rows = div_up(a.seq_len, parts);
   parts = div_up(a.seq_len, part_rows);
   return launch_kernel(router_backward_kernel<R, GATES>,
