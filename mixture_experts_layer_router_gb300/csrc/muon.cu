@@ -7,7 +7,8 @@
 // iteration is the published quintic one.
 //
 // Launches of one call: norm, init, and the iteration, whose last product
-// writes the caller's output or weights.
+// writes the caller's output or weights; or, for short sides up to 128, one
+// launch for everything.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -84,6 +85,7 @@ struct latentmoe_muon {
   NsArgs args;  // everything but the output and the tile shape
   lmoe::NsMaps maps;
   int pairs = 2;  // 0 single SMs, 1 SM pairs, 2 by the number of tiles
+  int small_ctas = 0, small_width = 0;  // the one-launch kernel's plan, 0: not for this size
   int64_t launches = 0;
   int last_cuda = 0;
 };
@@ -130,6 +132,34 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
   const lmoe::PdlScope pdl(true);
   const long long n = h->rows * h->cols;
   NsArgs& a = h->args;
+  if (h->small_ctas > 0 && h->pairs == 2) {
+    lmoe::NsSmallArgs t;
+    memset(&t, 0, sizeof(t));
+    t.g = u.g;
+    t.momentum = u.momentum;
+    t.g_f32 = u.g_f32 ? 1 : 0;
+    t.mu = u.mu;
+    t.nesterov = u.nesterov ? 1 : 0;
+    t.rows = a.rows;
+    t.cols = a.cols;
+    t.tall = a.tall;
+    t.m = a.side;
+    t.n = static_cast<int>(h->tall ? h->rows : h->cols);
+    t.width = h->small_width;
+    t.ctas = h->small_ctas;
+    t.steps = a.steps;
+    t.eps = h->eps;
+    t.scale0 = h->scale0;
+    t.out_mode = out_mode;
+    t.out = out;
+    t.keep = keep;
+    t.move = move;
+    t.status = a.status;
+    memcpy(t.step, a.step, sizeof(t.step));
+    NS_CK(h, lmoe::launch_ns_small(t, h->batch, s));
+    h->launches += 1;
+    return LATENTMOE_OK;
+  }
   NS_CK(h, lmoe::launch_ns_norm(u, h->batch, n, h->chunks, h->chunk, h->partial, s));
   NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, a.ld_x, h->chunks, h->partial,
                                 h->eps, h->scale0, h->x32, h->x16, a.done, 3 * a.steps, a.counter, s));
@@ -249,6 +279,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   h->chunks = static_cast<int>((n + chunk - 1) / chunk);
 
   cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = lmoe::ns_small_plan(R, C, &h->small_ctas, &h->small_width);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e != cudaSuccess) {

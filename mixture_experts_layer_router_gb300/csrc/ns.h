@@ -37,4 +37,34 @@ cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, l
 cudaError_t launch_ns_iterate(bool pair, const NsMaps& m, const NsArgs& a, int sms,
                               cudaStream_t s);
 
+// The one-launch kernel for short sides up to kSmallSide (ns_small.cuh).
+constexpr int kSmallSide = 128;
+constexpr int kSmallW = 256;  // columns a CTA, at most
+constexpr int kSmallCluster = 16;
+constexpr int kSmallThreads = 256;
+struct NsSmallArgs {
+  const void* g;
+  float* momentum;       // may be null
+  int g_f32;
+  float mu;
+  int nesterov;
+  int rows, cols, tall;
+  int m, n;              // short and long side
+  int width;             // columns of X a CTA, a multiple of 64
+  int ctas;              // of a cluster
+  int steps;
+  float eps, scale0;
+  int out_mode;
+  void* out;
+  float keep, move;
+  unsigned* status;
+  NsStep step[kNsMaxSteps];
+};
+
+// Whether the one-launch kernel takes matrices of this size (short side at most
+// 128, long side at most 4096): *ctas CTAs a matrix and *width columns of its
+// long side a CTA, or *ctas = 0.
+cudaError_t ns_small_plan(long long rows, long long cols, int* ctas, int* width);
+cudaError_t launch_ns_small(const NsSmallArgs& a, long long batch, cudaStream_t s);
+
 }  // namespace lmoe
