@@ -116,8 +116,8 @@ __device__ __forceinline__ void reduce_row(float (&v)[V], Op op) {
 
 // Exponentials as powers of two: exp(x - max) = 2^(c x - top) with c = log2 e and
 // top = c max rounded once, which is one fused multiply-add and one special
-// function. The rounding of top is common to a row: it cancels in p, and
-// lse = (top + log2(sum)) / c takes the same top. The special functions are the
+// function. The rounding of top is common to a row and cancels in p; in lse =
+// max + log2(sum) / c it is at most 2^-24 of |max|. The special functions are the
 // hardware's (2 ulp): errors of p and lse stay below 4e-6.
 constexpr float kLog2E = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
@@ -128,38 +128,56 @@ __device__ __forceinline__ float pow2(float x) {
 }
 __device__ __forceinline__ float recip(float x) { return __fdividef(1.0f, x); }
 
-// The tops of a batch's rows (0 for a row of -inf alone).
+// The maxima of a batch's rows (0 for a row of -inf alone).
 template <class R>
-__device__ __forceinline__ void row_tops(const float (&x)[R::U][R::N], float (&top)[R::U]) {
+struct Tops {
+  float max[R::U], top[R::U];
+  bool big;  // of the whole warp: some c max would overflow (a row masked with
+             // the type's lowest value); then the difference is taken first
+  __device__ __forceinline__ explicit Tops(const float (&x)[R::U][R::N]) {
 #pragma unroll
-  for (int u = 0; u < R::U; ++u) {
-    float m = x[u][0];
+    for (int u = 0; u < R::U; ++u) {
+      float m = x[u][0];
 #pragma unroll
-    for (int i = 1; i < R::N; ++i) m = fmaxf(m, x[u][i]);
-    top[u] = m;
+      for (int i = 1; i < R::N; ++i) m = fmaxf(m, x[u][i]);
+      max[u] = m;
+    }
+    reduce_row<R::LANES>(max, Max());
+    bool far = false;
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      if (max[u] == -INFINITY) max[u] = 0.0f;
+      top[u] = max[u] * kLog2E;
+      far |= fabsf(max[u]) > 1e37f;
+    }
+    big = __any_sync(0xffffffffu, far) != 0;
   }
-  reduce_row<R::LANES>(top, Max());
-#pragma unroll
-  for (int u = 0; u < R::U; ++u) top[u] = top[u] == -INFINITY ? 0.0f : top[u] * kLog2E;
-}
-// x <- 2^(c x - top); the lane's part of the sum. A row of -inf alone sums to 0,
-// a NaN makes its row's sum NaN.
-template <class R>
-__device__ __forceinline__ float row_exp(float (&x)[R::N], float top) {
-  float s = 0.0f, s2 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < R::N; i += 2) {
-    x[i] = pow2(fmaf(x[i], kLog2E, -top));
-    x[i + 1] = pow2(fmaf(x[i + 1], kLog2E, -top));
-    s += x[i];
-    s2 += x[i + 1];
+  __device__ __forceinline__ float exp(int u, float x) const {
+    return big ? pow2((x - max[u]) * kLog2E) : pow2(fmaf(x, kLog2E, -top[u]));
   }
-  return s + s2;
-}
-// lse of a row from its top and sum (>= about 1).
-__device__ __forceinline__ float row_lse(float top, float sum) {
-  return (top + __log2f(sum)) * kLn2;
-}
+  // x <- exp(x - max); the lane's part of the sum. A row of -inf alone sums to 0,
+  // a NaN makes its row's sum NaN.
+  __device__ __forceinline__ float exp_row(int u, float (&x)[R::N]) const {
+    float s = 0.0f, s2 = 0.0f;
+    if (big) {
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) x[i] = pow2((x[i] - max[u]) * kLog2E);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::N; ++i) x[i] = pow2(fmaf(x[i], kLog2E, -top[u]));
+    }
+#pragma unroll
+    for (int i = 0; i < R::N; i += 2) {
+      s += x[i];
+      s2 += x[i + 1];
+    }
+    return s + s2;
+  }
+  // log sum exp of a row from its sum (about 1 or more)
+  __device__ __forceinline__ float lse(int u, float sum) const {
+    return fmaf(__log2f(sum), kLn2, max[u]);
+  }
+};
 
 // Fixed-order sum over the block; every thread gets it. `buf`: kBalWarps floats.
 __device__ __forceinline__ float block_sum(float v, float* buf) {
@@ -261,10 +279,10 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     constexpr int kStride = kBalWarps * R::BATCH;
     int base = r0 + warp * R::BATCH;
     auto add = [&](LossRows<R>& cur) {
-      float top[R::U], sums[R::U];
-      row_tops<R>(cur.x, top);
+      const Tops<R> tops(cur.x);
+      float sums[R::U];
 #pragma unroll
-      for (int u = 0; u < R::U; ++u) sums[u] = row_exp<R>(cur.x[u], top[u]);
+      for (int u = 0; u < R::U; ++u) sums[u] = tops.exp_row(u, cur.x[u]);
       reduce_row<R::LANES>(sums, Add());
 #pragma unroll
       for (int u = 0; u < R::U; ++u) {
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
 #pragma unroll
           for (int i = 0; i < R::N; ++i) acc[i] = fmaf(cur.x[u][i], inv, acc[i]);
           if (q == 0) {
-            const float lse = row_lse(top[u], sum);
+            const float lse = tops.lse(u, sum);
             zsum = fmaf(lse, lse, zsum);
             ntok += 1;
           }
@@ -559,15 +577,14 @@ __global__ void __launch_bounds__(kBackThreads)
       cur.load(a, t0, base, r1, q, sub);
     }
     cur.gather(a, t0, base, sub);
-    float top[R::U];
-    row_tops<R>(cur.x, top);
+    const Tops<R> tops(cur.x);
 #pragma unroll
     for (int u = 0; u < R::U; ++u) {
       const long long t = t0 + base + u * R::ROWS + sub;
       // the row's sum and sum of w e; with gates also the sums of the choices'
       // e and of e dg
       float v[GATES ? 4 : 2];
-      v[0] = row_exp<R>(cur.x[u], top[u]);
+      v[0] = tops.exp_row(u, cur.x[u]);
       v[1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < R::N; ++i) v[1] = fmaf(cur.x[u][i], wt[i], v[1]);
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(kBackThreads)
         v[2] = v[3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < R::J; ++j) {
-          g[j] = cur.id[u][j] >= 0 ? pow2(fmaf(cur.xi[u][j], kLog2E, -top[u])) : 0.0f;
+          g[j] = cur.id[u][j] >= 0 ? tops.exp(u, cur.xi[u][j]) : 0.0f;
           v[2] += g[j];
           v[3] = fmaf(g[j], cur.dg[u][j], v[3]);
         }
@@ -587,7 +604,7 @@ __global__ void __launch_bounds__(kBackThreads)
       const float inv = empty ? 0.0f : recip(sum);
       // p_e (wt_e + shift)
       const bool on = cur.in[u] && cur.valid[u] != 0 && !empty;
-      float shift = on ? fmaf(zq, row_lse(top[u], sum), -v[1] * inv) : 0.0f;
+      float shift = on ? fmaf(zq, tops.lse(u, sum), -v[1] * inv) : 0.0f;
       float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
       if constexpr (GATES) {
         float gs = v[2], gd = v[3], ginv = inv;
@@ -599,11 +616,11 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
             for (int j = 1; j < R::J; ++j) m[0] = fmaxf(m[0], cur.xi[u][j]);
             reduce_row<R::LANES>(m, Max());
-            const float own = m[0] == -INFINITY ? 0.0f : m[0] * kLog2E;
+            const float own = m[0] == -INFINITY ? 0.0f : m[0];
             float w[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < R::J; ++j) {
-              g[j] = cur.id[u][j] >= 0 ? pow2(fmaf(cur.xi[u][j], kLog2E, -own)) : 0.0f;
+              g[j] = cur.id[u][j] >= 0 ? pow2((cur.xi[u][j] - own) * kLog2E) : 0.0f;
               w[0] += g[j];
               w[1] = fmaf(g[j], cur.dg[u][j], w[1]);
             }

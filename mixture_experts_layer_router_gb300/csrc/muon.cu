@@ -111,19 +111,21 @@ long long tiles(long long M, long long N, long long bt) {
   return ((M + bt - 1) / bt) * ((N + bt - 1) / bt);
 }
 
-// SM pairs (256 x 256 tiles) or single SMs (128 x 128)? A single tile's k-block
-// takes about as long as a pair tile's once all SMs run (both are then bound by
-// operand traffic from L2; 560 and 600 clocks measured), so the fewer rounds of
-// tiles decide, weighted with the k-blocks of each product.
+// SM pairs (256 x 256 tiles) or single SMs (128 x 128)? A k-block takes about
+// 0.3 us in either kind of tile (a single SM's is bound by the latency of its
+// operands, a pair's by the tensor cores), a phase's hand-over 5.5 us with single
+// tiles and 8.5 with pair tiles, whose CTAs have twice the results to store: 18
+// and 27 k-blocks. Measured, single against pair: 3 x 777 x 1333 211 and 238 us,
+// 1024 x 1024 163 and 203, 2048 x 2048 310 and 298, 8 x 1024 x 2048 469 and 392.
 bool use_pairs(const latentmoe_muon* h) {
   if (h->pairs != 2) return h->pairs == 1;
-  const long long m = h->side, n = h->tall ? h->rows : h->cols;
-  const auto rounds = [&](long long bt, long long units) {
-    const long long sym = (sym_tiles(m, bt) * h->batch + units - 1) / units;
-    const long long app = (tiles(m, n, bt) * h->batch + units - 1) / units;
-    return sym * (n + m) + app * m;
+  const NsArgs& a = h->args;
+  const auto cost = [&](long long bt, long long units, long long hand_over) {
+    const long long sym = (sym_tiles(h->side, bt) * h->batch + units - 1) / units;
+    const long long app = (tiles(h->rows, h->cols, bt) * h->batch + units - 1) / units;
+    return sym * (a.k_gram + a.k_side) + app * a.k_side + 3 * hand_over;
   };
-  return h->sms >= 2 && rounds(256, h->sms / 2) < rounds(128, h->sms);
+  return h->sms >= 2 && cost(256, h->sms / 2, 27) < cost(128, h->sms, 18);
 }
 
 // The whole iteration on U; the last product writes `out` as out_mode says.

@@ -386,17 +386,20 @@ __device__ __forceinline__ void ns_put_out(const NsArgs& a, int b, uint8_t* slot
   if (a.out_mode == kNsOutWeightF32) {
     float* w = reinterpret_cast<float*>(a.out) + at0;
     if (whole) {
-      float4 o[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < rows) o[q] = *reinterpret_cast<const float4*>(w + q * step);
+      for (int q0 = 0; q0 < 8; q0 += 4) {
+        float4 o[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (q < rows) {
-          const float4 x = value(q);
-          *reinterpret_cast<float4*>(w + q * step) =
-              make_float4(fmaf(a.keep, o[q].x, -a.move * x.x), fmaf(a.keep, o[q].y, -a.move * x.y),
-                          fmaf(a.keep, o[q].z, -a.move * x.z), fmaf(a.keep, o[q].w, -a.move * x.w));
+        for (int q = 0; q < 4; ++q)
+          if (q0 + q < rows) o[q] = *reinterpret_cast<const float4*>(w + (q0 + q) * step);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q0 + q < rows) {
+            const float4 x = value(q0 + q);
+            *reinterpret_cast<float4*>(w + (q0 + q) * step) = make_float4(
+                fmaf(a.keep, o[q].x, -a.move * x.x), fmaf(a.keep, o[q].y, -a.move * x.y),
+                fmaf(a.keep, o[q].z, -a.move * x.z), fmaf(a.keep, o[q].w, -a.move * x.w));
+          }
         }
       }
     } else {
@@ -413,24 +416,27 @@ __device__ __forceinline__ void ns_put_out(const NsArgs& a, int b, uint8_t* slot
   __nv_bfloat16* w = reinterpret_cast<__nv_bfloat16*>(a.out) + at0;
   const bool weight = a.out_mode == kNsOutWeightBf16;
   if (whole) {
-    uint2 o[8];
-    if (weight) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < rows) o[q] = *reinterpret_cast<const uint2*>(w + q * step);
-    }
+    for (int q0 = 0; q0 < 8; q0 += 4) {
+      uint2 o[4];
+      if (weight) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (q < rows) {
-        float4 x = value(q);
-        if (weight) {
-          x.x = fmaf(a.keep, __uint_as_float(o[q].x << 16), -a.move * x.x);
-          x.y = fmaf(a.keep, __uint_as_float(o[q].x & 0xffff0000u), -a.move * x.y);
-          x.z = fmaf(a.keep, __uint_as_float(o[q].y << 16), -a.move * x.z);
-          x.w = fmaf(a.keep, __uint_as_float(o[q].y & 0xffff0000u), -a.move * x.w);
+        for (int q = 0; q < 4; ++q)
+          if (q0 + q < rows) o[q] = *reinterpret_cast<const uint2*>(w + (q0 + q) * step);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q0 + q < rows) {
+          float4 x = value(q0 + q);
+          if (weight) {
+            x.x = fmaf(a.keep, __uint_as_float(o[q].x << 16), -a.move * x.x);
+            x.y = fmaf(a.keep, __uint_as_float(o[q].x & 0xffff0000u), -a.move * x.y);
+            x.z = fmaf(a.keep, __uint_as_float(o[q].y << 16), -a.move * x.z);
+            x.w = fmaf(a.keep, __uint_as_float(o[q].y & 0xffff0000u), -a.move * x.w);
+          }
+          *reinterpret_cast<uint2*>(w + (q0 + q) * step) =
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
         }
-        *reinterpret_cast<uint2*>(w + q * step) =
-            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
       }
     }
   } else {
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     const uint64_t t0 = global_timer_ns();
     uint32_t n = 0;
     while (true) {
-      __nanosleep(64);
+      __nanosleep(20);
       if (ld_acquire_gpu(p) >= want) return true;
       if ((++n & 31u) == 0) {
         if (*abort_flag) return false;
@@ -574,6 +580,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     fence_mbar_init();
     fence_async_smem();
   }
+  if (warp == 2 && lane < sizeof(NsMaps) / sizeof(CUtensorMap))
+    tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&tm) + lane);
   __syncwarp();
   if (warp == 1) {
     if constexpr (PAIR) {

@@ -151,3 +151,270 @@ def test_loss_and_backward(T, E, k, pad):
         check_backward(L, logits, idx, valid, 0, None, got, renorm,
                        d_loss=torch.tensor([2.5], device="cuda"))
         assert L.status() == 0
+
+
+@pytest.mark.parametrize("S,L,E,k", [(2, 1, 5, 2), (3, 5, 16, 2), (16, 64, 64, 4), (200, 7, 60, 6),
+                                     (2, 5000, 32, 4), (9, 33, 512, 8), (40, 700, 256, 7),
+                                     (152, 3, 8, 8), (1, 6001, 13, 1)])
+def test_sequences(S, L, E, k):
+    T = S * L
+    for renorm in (False, True):
+        h = layer(E, k, T, renorm)
+        logits, idx, valid, dg = inputs(T, E, k, T + E, scale=2.0, pad=True)
+        valid.view(S, L)[0] = 0  # a sequence of padding alone
+        got = check_loss(h, logits, idx, valid, L, T)
+        assert int(got["tokens"][0]) == 0 and not bool(got["counts"][0].any())
+        check_backward(h, logits, idx, valid, L, dg, got, renorm,
+                       d_loss=torch.tensor([0.5], device="cuda"))
+        assert h.status() == 0
+
+
+def test_nothing_counts():
+    h = layer(16, 2, 64)
+    logits, idx, _, dg = inputs(64, 16, 2, 5)
+    valid = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    logits[3] = float("nan")  # padding may hold anything
+    got = h.balance_loss(logits, idx, valid=valid, balance_coef=BC, z_coef=ZC)
+    for key in got:
+        assert not bool(got[key].any()), key
+    out = h.router_backward(logits, idx, got["counts"], got["tokens"], valid=valid,
+                            balance_coef=BC, z_coef=ZC)
+    assert torch.equal(out, torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 6), (64, 4), (512, 8)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_masked_logits(E, k, renorm):
+    """Masks of -inf and of the type's lowest value: some experts, whole rows."""
+    T = 96
+    h = layer(E, k, T, renorm)
+    logits, idx, _, dg = inputs(T, E, k, 11)
+    low = torch.finfo(torch.float32).min
+    logits[0] = float("-inf")           # nothing left: the row does not count
+    logits[1] = low                     # equal lowest values: uniform
+    logits[2, : E // 2] = float("-inf")
+    logits[3, : E // 2] = low
+    logits[4, 1:] = float("-inf")       # one expert left
+    logits[5] = 3.0e38                  # the other end
+    logits[6] *= 1e4
+    logits[7] = logits[7] * 1e-30 + 80.0
+    # row 1's and 5's z terms overflow by definition; they are checked apart
+    z_rows = torch.ones(T, dtype=torch.uint8, device="cuda")
+    z_rows[1] = z_rows[5] = 0
+    got = check_loss(h, logits, idx, z_rows, 0, T)
+    assert int(got["tokens"]) == T - 3
+    check_backward(h, logits, idx, z_rows, 0, dg, got, renorm)
+    one = h.balance_loss(logits, idx, balance_coef=1.0, z_coef=0.0)
+    p = torch.softmax(logits.double(), 1)
+    p[0] = 0
+    assert int(one["tokens"]) == T - 1
+    assert rel(one["prob_sum"][0], p.sum(0)) <= P_TOL
+    assert torch.isinf(one["z_sum"]).all()
+
+
+def test_nan_is_not_hidden():
+    h = layer(32, 4, 50)
+    logits, idx, _, dg = inputs(50, 32, 4, 3)
+    logits[7, 5] = float("nan")
+    got = h.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+    assert torch.isnan(got["loss"]).all() and int(got["tokens"]) == 50
+    out = h.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg,
+                            balance_coef=BC, z_coef=ZC)
+    bad = torch.isnan(out).any(1)
+    assert bool(bad[7]) and int(bad.sum()) == 1
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(8, 4), (64, 4), (13, 6), (256, 16)])
+def test_given_choices(E, k, renorm):
+    """Replayed choices: repeated ids add up, ids outside [0, E) drop out, ids of
+    vanishing probability keep their renormalised gates."""
+    T = 70
+    h = layer(E, k, T, renorm)
+    logits, idx, _, dg = inputs(T, E, k, 17)
+    idx[0] = idx[0, 0]
+    idx[1, 1] = idx[1, 0]
+    idx[2, 0] = -1
+    idx[3, k - 1] = E
+    idx[4] = 1 << 30
+    idx[5, 0] = -(1 << 31)
+    logits[6] += 200.0 * (torch.arange(E, device="cuda") == E - 1)
+    idx[6] = torch.arange(k, device="cuda") % (E - 1)
+    got = check_loss(h, logits, idx, None, 0, T)
+    assert h.status() == capi.STATUS_BAD_EXPERT
+    assert h.status() == 0
+    check_backward(h, logits, idx, None, 0, dg, got, renorm)
+    a = h.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg)
+    for _ in range(3):
+        assert torch.equal(a, h.router_backward(logits, idx, got["counts"], got["tokens"],
+                                                d_gates=dg))
+
+
+@pytest.mark.parametrize("E,ld,ldd", [(64, 80, 64), (64, 67, 72), (60, 61, 60), (512, 516, 520)])
+def test_row_strides_and_in_place(E, ld, ldd):
+    T, k = 130, 4
+    h = layer(E, k, T)
+    logits, idx, _, dg = inputs(T, E, k, 23)
+    wide = torch.full((T, ld), 1e9, device="cuda")
+    wide[:, :E] = logits
+    view = wide[:, :E]
+    got = h.balance_loss(view, idx, balance_coef=BC, z_coef=ZC)
+    plain = h.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+    assert torch.equal(got["counts"], plain["counts"])
+    assert rel(got["loss"], plain["loss"].double()) <= L_TOL
+    out = torch.full((T, ldd), 7.0, device="cuda")
+    args = dict(d_gates=dg, balance_coef=BC, z_coef=ZC)
+    h.router_backward(view, idx, got["counts"], got["tokens"], out=out[:, :E], **args)
+    assert torch.all(out[:, E:] == 7.0) and torch.all(wide[:, E:] == 1e9)
+    want = h.router_backward(logits, idx, got["counts"], got["tokens"], **args)
+    torch.testing.assert_close(out[:, :E], want, rtol=1e-5, atol=1e-9)
+    same = logits.clone()
+    h.router_backward(same, idx, got["counts"], got["tokens"], out=same, **args)
+    assert torch.equal(same, want)
+
+
+def test_sums_of_micro_batches():
+    """The stats of two halves add up to the whole batch's; the loss of the sums
+    and the gradient with the sums are the whole batch's."""
+    T, E, k = 1000, 64, 4
+    h = layer(E, k, T)
+    logits, idx, valid, dg = inputs(T, E, k, 31, pad=True)
+    whole = h.balance_loss(logits, idx, valid=valid, balance_coef=BC, z_coef=ZC)
+    cut = 360
+    halves = [h.balance_loss(logits[a:b], idx[a:b], valid=valid[a:b]) for a, b in
+              ((0, cut), (cut, T))]
+    total = {n: halves[0][n] + halves[1][n] for n in ("counts", "prob_sum", "z_sum", "tokens")}
+    assert torch.equal(total["counts"], whole["counts"])
+    loss = h.balance_loss_from_stats(total, balance_coef=BC, z_coef=ZC)
+    assert rel(loss, whole["loss"].double()) <= L_TOL
+    d = h.router_backward(logits, idx, whole["counts"], whole["tokens"], d_gates=dg, valid=valid,
+                          balance_coef=BC, z_coef=ZC)
+    parts = [h.router_backward(logits[a:b], idx[a:b], total["counts"], total["tokens"],
+                               d_gates=dg[a:b], valid=valid[a:b], balance_coef=BC, z_coef=ZC)
+             for a, b in ((0, cut), (cut, T))]
+    assert torch.equal(d, torch.cat(parts))
+    seqs = h.balance_loss(logits, idx, valid=valid, seq_len=100, balance_coef=BC, z_coef=ZC)
+    again = h.balance_loss_from_stats(seqs, balance_coef=BC, z_coef=ZC)
+    assert rel(again, seqs["loss"].double()) <= L_TOL
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_by_differences(renorm):
+    """<gradient, v> against central differences of the float64 definition along
+    v. The definition is smooth: a step of 1e-4 leaves an error of order 1e-8;
+    the gradient's own is 1e-5 of the sum of its absolute terms."""
+    T, E, k, S = 24, 20, 3, 2
+    h = layer(E, k, T, renorm)
+    logits, idx, valid, dg = inputs(T, E, k, 41, pad=True)
+    got = h.balance_loss(logits, idx, valid=valid, seq_len=T // S, balance_coef=BC, z_coef=ZC)
+    d = h.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg, valid=valid,
+                          seq_len=T // S, balance_coef=BC, z_coef=ZC).double()
+
+    def f(x):
+        return definition(x, idx, valid, S)["loss"][0] + (gates_of(x, idx, renorm) *
+                                                          dg.double()).sum()
+
+    for seed in range(5):
+        v = torch.randn((T, E), generator=torch.Generator().manual_seed(seed),
+                        dtype=torch.float64).cuda()
+        e = 1e-4
+        diff = (f(logits.double() + e * v) - f(logits.double() - e * v)) / (2 * e)
+        assert abs(float((d * v).sum() - diff)) <= 1e-5 * float((d * v).abs().sum()) + 1e-6
+
+
+def test_other_stream_and_graph():
+    T, E, k = 4096, 64, 4
+    h = layer(E, k, T)
+    logits, idx, _, dg = inputs(T, E, k, 47)
+    want = h.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+    d = h.router_backward(logits, idx, want["counts"], want["tokens"], d_gates=dg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = h.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+        e = h.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg)
+    side.synchronize()
+    for key in want:
+        assert torch.equal(want[key], got[key]), key
+    assert torch.equal(d, e)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = h.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+        e = h.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg)
+    before = h.launch_count()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert h.launch_count() == before
+    for key in want:
+        assert torch.equal(want[key], got[key]), key
+    assert torch.equal(d, e)
+
+
+def test_matches_the_forwards_statistics():
+    """On the routing of a forward: the statistics of latentmoe_lbl_stats."""
+    from mixture_experts_layer_router_gb300 import synth
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.make_weights(cfg, 2, "cuda")
+    h = gh.make_layer(cfg, w)
+    h.forward(synth.make_x(cfg, 2, "cuda"))
+    r = h.get_routing(cfg.T, "cuda")
+    prob, counts = h.lbl_stats("cuda")
+    got = h.balance_loss(r["logits"], r["idx"])
+    assert torch.equal(got["counts"][0], counts)
+    assert rel(got["prob_sum"][0], prob.double()) <= 2 * P_TOL
+    assert int(got["tokens"]) == cfg.T
+
+
+def test_refusals():
+    T, E, k = 64, 16, 2
+    h = layer(E, k, T)
+    logits, idx, _, dg = inputs(T, E, k, 1)
+    got = h.balance_loss(logits, idx)
+    lib, hd = capi.load(), h.handle
+    st = capi.latentmoe_balance_stats(*(got[n].data_ptr() for n in
+                                        ("counts", "prob_sum", "z_sum", "tokens")))
+    loss = torch.empty(3, device="cuda")
+    import ctypes
+
+    def fwd(T_=T, ld=E, seq=0, p=logits.data_ptr(), bc=1.0, i=idx.data_ptr(), o=loss.data_ptr()):
+        return lib.latentmoe_balance_loss(hd, p, ld, i, None, T_, seq, bc, 0.0, ctypes.byref(st),
+                                          o, None)
+
+    assert fwd() == capi.OK
+    assert fwd(T_=0) == fwd(T_=-1) == fwd(T_=T + 1) == capi.ERR_INVALID_ARG
+    assert fwd(seq=7) == fwd(seq=-1) == capi.ERR_INVALID_ARG
+    assert fwd(ld=E - 1) == capi.ERR_INVALID_ARG
+    assert fwd(p=None) == fwd(i=None) == fwd(o=None) == capi.ERR_INVALID_ARG
+    assert fwd(bc=float("nan")) == capi.ERR_INVALID_ARG
+    assert fwd(p=logits.data_ptr() + 4, T_=1) == capi.ERR_UNSUPPORTED
+    out = torch.empty_like(logits)
+
+    def bwd(c=got["counts"].data_ptr(), n=got["tokens"].data_ptr(), i=idx.data_ptr(),
+            g=dg.data_ptr(), o=out.data_ptr(), ldd=E, seq=0):
+        return lib.latentmoe_router_backward(hd, logits.data_ptr(), E, i, g, None, c, n, T, seq,
+                                             1.0, 0.0, None, o, ldd, None)
+
+    assert bwd() == bwd(g=None, i=None) == capi.OK
+    assert bwd(c=None) == bwd(n=None) == bwd(o=None) == bwd(i=None) == capi.ERR_INVALID_ARG
+    assert bwd(ldd=E - 1) == bwd(seq=5) == capi.ERR_INVALID_ARG
+    assert bwd(o=out.data_ptr() + 4) == capi.ERR_UNSUPPORTED
+    assert lib.latentmoe_balance_loss_from_stats(hd, ctypes.byref(st), 0, 1.0, 0.0,
+                                                 loss.data_ptr(), None) == capi.ERR_INVALID_ARG
+    st.counts = None
+    assert fwd() == capi.ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    # the binding's own checks
+    for bad in (dict(logits=logits.double()), dict(logits=logits[:, :8]), dict(idx=idx.long()),
+                dict(idx=idx[:10]), dict(seq_len=7), dict(valid=torch.ones(T, device="cuda")),
+                dict(logits=logits.t().contiguous().t()), dict(logits=logits.cpu())):
+        args = dict(logits=logits, idx=idx)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            h.balance_loss(**args)
+    for bad in (dict(counts=got["counts"].long()), dict(tokens=got["tokens"][:0]),
+                dict(d_gates=dg.half()), dict(d_loss=torch.ones(2, device="cuda"))):
+        args = dict(logits=logits, idx=idx, counts=got["counts"], tokens=got["tokens"])
+        args.update(bad)
+        with pytest.raises(ValueError):
+            h.router_backward(**args)
