@@ -522,8 +522,9 @@ typedef struct latentmoe_muon* latentmoe_muon_t;
 enum { LATENTMOE_BF16 = 0, LATENTMOE_FP32 = 1 }; /* element types of g and w below */
 
 /* batch 1..65535, rows and cols 1..65536 (any size: no multiples needed),
- * steps 1..32. coefs: host [steps][3] = (a, b, c) of each step, or NULL for
- * (3.4445, -4.7750, 2.0315) in every step. eps >= 1e-30. */
+ * steps 1..32. coefs: host [steps][3] = (a, b, c) of each step, with
+ * 64 |a| >= |b| + |c|, or NULL for (3.4445, -4.7750, 2.0315) in every step.
+ * eps >= 1e-30. */
 typedef struct {
   int64_t batch;
   int64_t rows;
@@ -554,8 +555,8 @@ typedef struct {
  * about 8 rows cols + 4 min(rows, cols)^2 bytes). The handle follows the rules of a
  * layer handle: one host thread and one stream at a time, one device.
  * Errors: INVALID_ARG (NULL, a size or steps < 1, eps out of range,
- * coefficients that are not finite or under which a singular value in [0, 1]
- * grows beyond 1e6), UNSUPPORTED (beyond the limits above), OUT_OF_MEMORY,
+ * coefficients that are not finite, lack the linear term asked for above or
+ * let a singular value in [0, 1] grow beyond 1e6), UNSUPPORTED (beyond the limits above), OUT_OF_MEMORY,
  * CUDA. On error *out is NULL and nothing stays allocated. */
 int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out);
 

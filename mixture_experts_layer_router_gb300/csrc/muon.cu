@@ -208,6 +208,9 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
     const float cb = d.coefs ? d.coefs[3 * i + 1] : -4.7750f;
     const float cc = d.coefs ? d.coefs[3 * i + 2] : 2.0315f;
     if (!isfinite(ca) || !isfinite(cb) || !isfinite(cc)) return LATENTMOE_ERR_INVALID_ARG;
+    // the scales come from the largest possible singular value: directions far
+    // below it, whose A^2 underflows, are right only through their a X
+    if (!(fabsf(ca) * 64.0f >= fabsf(cb) + fabsf(cc))) return LATENTMOE_ERR_INVALID_ARG;
     double next = 0.0, poly = 0.0;
     for (int j = 0; j <= 1024; ++j) {
       const double x = u * j / 1024.0, x2 = x * x;

@@ -21,9 +21,10 @@
 //   entries once X's singular values draw together, are fp32 vectors that the
 //   epilogues apply (A A = A' A' + (d_i + d_j) A' + d d, with A' = A less its
 //   diagonal d). That takes the error from 1.2e-3..2.0e-3 to 2e-4..7e-4. In the
-//   first two steps P keeps its diagonal in fp16: there it has to cancel against
-//   the off-diagonal part in the directions where P X is small (low rank:
-//   1.2e-3..3e-3 with an exact diagonal, 2e-4..9e-4 so).
+//   first two steps P keeps its diagonal in fp16 (the vector holds what the
+//   rounding left): there it has to cancel against the off-diagonal part in the
+//   directions where P X is small (low rank: 1.2e-3..3e-3 with the whole
+//   diagonal apart, 2e-4..9e-4 so).
 //
 // X keeps the caller's orientation. Where the contracted index is X's row
 // index, X is read as an MN-major operand (TMA boxes of 64 contiguous columns x
@@ -328,7 +329,7 @@ __device__ __forceinline__ void ns_sym_chunk(const NsArgs& a, const NsStep& f, c
     __half h = __float2half_rn(0.0f);
     if (poly && c.step < kNsEarly) {
       h = __float2half_rn(d * f.s_p);
-      d = 0.0f;
+      d -= __half2float(h) / f.s_p;  // what the rounding left
     }
     reinterpret_cast<__half*>(half_at(slot, lane, lane >> 3))[lane & 7] = h;
     (poly ? a.diag_p : a.diag_a)[c.b * a.ld_a + row + lane] = d;

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
           __half h = __float2half_rn(0.0f);
           if (s < kNsEarly) {
             h = __float2half_rn(d * f.s_p);
-            d = 0.0f;
+            d -= __half2float(h) / f.s_p;  // what the rounding left
           }
           *reinterpret_cast<__half*>(pop + op_at(row, row >> 3) + (row & 7) * 2) = h;
           diag_p[row] = d;

@@ -33,9 +33,10 @@ def test_muon_create_refuses(lib, kw, code):
 
 
 @pytest.mark.parametrize("coefs", [[math.nan, 0, 0], [math.inf, 0, 0], [1e9, 0, 0],
-                                   [4.0, 0.0, 0.0]])
+                                   [4.0, 0.0, 0.0], [0.0, 0.0, 1.0], [0.01, -1.0, 0.0]])
 def test_muon_create_refuses_coefficients(lib, coefs):
-    """Not finite, or growing without bound (4^32 in 32 steps)."""
+    """Not finite, growing without bound (4^32 in 32 steps), or without a linear
+    term (X to the fifth power leaves the range that the scales are made for)."""
     arr = (ctypes.c_float * 96)(*(coefs * 32))
     h = ctypes.c_void_p(7)
     d = dims(steps=32, coefs=ctypes.cast(arr, ctypes.POINTER(ctypes.c_float)))
