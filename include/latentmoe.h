@@ -562,8 +562,8 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
 
 /* out (bf16) = the iteration's X for U = g; g of type g_dtype; both
  * contiguous device [batch, rows, cols]. out may be g itself if g is bf16,
- * and may not overlap it otherwise. Asynchronous on `stream`, 3 launches, no
- * host synchronisation: it can be captured into a CUDA graph once a first
+ * and may not overlap it otherwise. Asynchronous on `stream`, 3 launches (1
+ * for small matrices, see latentmoe_muon_set_sm_pairs), no host synchronisation: it can be captured into a CUDA graph once a first
  * call outside the capture has set up the kernels. Errors:
  * INVALID_ARG (NULL, unknown type), UNSUPPORTED (pointer not 16-byte
  * aligned), CUDA. */
@@ -577,7 +577,9 @@ int latentmoe_muon_step(latentmoe_muon_t h, const latentmoe_muon_update* u,
                         latentmoe_stream_t stream);
 
 /* Tiles of the products: 0 = 128 x 128 on single SMs, 1 = 256 x 256 on SM
- * pairs, 2 (the default) = whichever takes fewer rounds of tiles. */
+ * pairs, 3 = 128 x 64 on single SMs, 2 (the default) = whichever is expected
+ * to take the least time; matrices with a short side of at most 128 and a long
+ * one of at most 4096 then run in one launch without tiles. */
 int latentmoe_muon_set_sm_pairs(latentmoe_muon_t h, int mode);
 
 /* As latentmoe_get_status, latentmoe_get_launch_count, latentmoe_last_cuda_error

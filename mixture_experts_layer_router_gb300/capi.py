@@ -625,7 +625,8 @@ class Muon:
                     "latentmoe_muon_step")
 
     def set_sm_pairs(self, mode: int) -> None:
-        """0: 128 x 128 tiles on single SMs; 1: 256 x 256 on SM pairs; 2: automatic."""
+        """0: 128 x 128 tiles on single SMs; 1: 256 x 256 on SM pairs; 3: 128 x 64
+        on single SMs; 2: automatic."""
         self._check(load().latentmoe_muon_set_sm_pairs(self.handle, int(mode)),
                     "latentmoe_muon_set_sm_pairs")
 

@@ -84,7 +84,7 @@ struct latentmoe_muon {
   __half* x16 = nullptr;  // the first X
   NsArgs args;  // everything but the output and the tile shape
   lmoe::NsMaps maps;
-  int pairs = 2;  // 0 single SMs, 1 SM pairs, 2 by the number of tiles
+  int pairs = 2;  // 0 single, 1 pair, 2 by the number of tiles, 3 narrow
   int small_ctas = 0, small_width = 0;  // the one-launch kernel's plan, 0: not for this size
   int64_t launches = 0;
   int last_cuda = 0;
@@ -103,29 +103,37 @@ int fail(latentmoe_muon* h, cudaError_t e) {
     if (e_ != cudaSuccess) return fail(h, e_);  \
   } while (0)
 
-long long sym_tiles(long long m, long long bt) {
-  const long long t = (m + bt - 1) / bt;
-  return t * (t + 1) / 2;
+// Tiles of a symmetric m x m result (on and below the diagonal) and of an M x N one.
+long long sym_tiles(long long m, int shape) {
+  const long long t = (m + lmoe::ns_bm(shape) - 1) / lmoe::ns_bm(shape);
+  return t * (t + 1) / 2 * (lmoe::ns_bm(shape) / lmoe::ns_bn(shape));
 }
-long long tiles(long long M, long long N, long long bt) {
-  return ((M + bt - 1) / bt) * ((N + bt - 1) / bt);
+long long tiles(long long M, long long N, int shape) {
+  const long long bm = lmoe::ns_bm(shape), bn = lmoe::ns_bn(shape);
+  return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
 }
 
-// SM pairs (256 x 256 tiles) or single SMs (128 x 128)? A k-block takes about
-// 0.3 us in either kind of tile (a single SM's is bound by the latency of its
-// operands, a pair's by the tensor cores), a phase's hand-over 5.5 us with single
-// tiles and 8.5 with pair tiles, whose CTAs have twice the results to store: 18
-// and 27 k-blocks. Measured, single against pair: 3 x 777 x 1333 211 and 238 us,
-// 1024 x 1024 163 and 203, 2048 x 2048 310 and 298, 8 x 1024 x 2048 469 and 392.
-bool use_pairs(const latentmoe_muon* h) {
-  if (h->pairs != 2) return h->pairs == 1;
+// Rounds of tiles decide the shape: a round takes its k-blocks and, once a phase,
+// the hand-over of the results to the next phase. In ns, measured: a k-block 270
+// (narrow), 320 (single), 310 (pair): an SM takes in about 64 bytes a clock, which
+// bounds the first two; a hand-over 4200, 5400, 8400. Whole calls in us, narrow /
+// single / pair: 512 x 512 103 / 124 / 162, 1024 x 1024 147 / 163 / 202, 3 x 777 x
+// 1333 220 / 213 / 238, 2048 x 2048 471 / 314 / 298, 8 x 1024 x 2048 732 / 470 / 394.
+int pick_shape(const latentmoe_muon* h) {
+  if (h->pairs != 2)
+    return h->pairs == 0 ? lmoe::kNsSingle : h->pairs == 1 ? lmoe::kNsPair : lmoe::kNsNarrow;
   const NsArgs& a = h->args;
-  const auto cost = [&](long long bt, long long units, long long hand_over) {
-    const long long sym = (sym_tiles(h->side, bt) * h->batch + units - 1) / units;
-    const long long app = (tiles(h->rows, h->cols, bt) * h->batch + units - 1) / units;
-    return sym * (a.k_gram + a.k_side) + app * a.k_side + 3 * hand_over;
+  const auto cost = [&](int shape, long long units, long long block, long long hand_over) {
+    const long long sym = (sym_tiles(h->side, shape) * h->batch + units - 1) / units;
+    const long long app = (tiles(h->rows, h->cols, shape) * h->batch + units - 1) / units;
+    return (sym * (a.k_gram + a.k_side) + app * a.k_side) * block + 3 * hand_over;
   };
-  return h->sms >= 2 && cost(256, h->sms / 2, 27) < cost(128, h->sms, 18);
+  const long long narrow = cost(lmoe::kNsNarrow, h->sms, 270, 4200);
+  const long long single = cost(lmoe::kNsSingle, h->sms, 320, 5400);
+  const long long pair =
+      h->sms >= 2 ? cost(lmoe::kNsPair, h->sms / 2, 310, 8400) : single + narrow;
+  if (pair < single && pair < narrow) return lmoe::kNsPair;
+  return narrow < single ? lmoe::kNsNarrow : lmoe::kNsSingle;
 }
 
 // The whole iteration on U; the last product writes `out` as out_mode says.
@@ -166,17 +174,17 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
   NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, a.ld_x, h->chunks, h->partial,
                                 h->eps, h->scale0, h->x32, h->x16, a.done, 3 * a.steps, a.counter, s));
   h->launches += 2;
-  const bool pair = use_pairs(h);
-  const long long bt = pair ? 256 : 128;
-  a.sym_tiles = static_cast<int>(sym_tiles(h->side, bt));
-  a.m_tiles = static_cast<int>((h->rows + bt - 1) / bt);
-  a.apply_tiles = static_cast<int>(tiles(h->rows, h->cols, bt));
+  const int shape = pick_shape(h);
+  const long long bm = lmoe::ns_bm(shape);
+  a.sym_tiles = static_cast<int>(sym_tiles(h->side, shape));
+  a.m_tiles = static_cast<int>((h->rows + bm - 1) / bm);
+  a.apply_tiles = static_cast<int>(tiles(h->rows, h->cols, shape));
   a.group = h->group;
   a.out_mode = out_mode;
   a.out = out;
   a.keep = keep;
   a.move = move;
-  NS_CK(h, lmoe::launch_ns_iterate(pair, h->maps, a, h->sms, s));
+  NS_CK(h, lmoe::launch_ns_iterate(shape, h->maps, a, h->sms, s));
   h->launches += 1;
   return LATENTMOE_OK;
 }
@@ -244,7 +252,8 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   const long long side = R < C ? R : C;
   const long long ldx = (C + 7) / 8 * 8, lda = (side + 7) / 8 * 8;
   // positions in the tile sequence stay in int
-  if ((2 * sym_tiles(side, 128) + tiles(R, C, 128)) * B * d.steps > (1ll << 30))
+  if ((2 * sym_tiles(side, lmoe::kNsNarrow) + tiles(R, C, lmoe::kNsNarrow)) * B * d.steps >
+      (1ll << 30))
     return LATENTMOE_ERR_UNSUPPORTED;
 
   latentmoe_muon* h = new (std::nothrow) latentmoe_muon();
@@ -383,7 +392,7 @@ int latentmoe_muon_step(latentmoe_muon_t h, const latentmoe_muon_update* p,
 }
 
 int latentmoe_muon_set_sm_pairs(latentmoe_muon_t h, int mode) {
-  if (h == nullptr || mode < 0 || mode > 2) return LATENTMOE_ERR_INVALID_ARG;
+  if (h == nullptr || mode < 0 || mode > 3) return LATENTMOE_ERR_INVALID_ARG;
   h->pairs = mode;
   return LATENTMOE_OK;
 }

@@ -32,9 +32,8 @@ cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, l
                            float* x32, __half* x16, int* done, int phases, int* counter,
                            cudaStream_t s);
 
-// All steps in one launch. pair: tiles of 256 x 256 on SM pairs instead of
-// 128 x 128 on single SMs.
-cudaError_t launch_ns_iterate(bool pair, const NsMaps& m, const NsArgs& a, int sms,
+// All steps in one launch, on tiles of a shape (NsShape).
+cudaError_t launch_ns_iterate(int shape, const NsMaps& m, const NsArgs& a, int sms,
                               cudaStream_t s);
 
 // The one-launch kernel for short sides up to kSmallSide (ns_small.cuh).

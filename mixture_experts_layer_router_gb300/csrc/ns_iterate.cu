@@ -4,15 +4,16 @@
 
 namespace lmoe {
 
-template <bool PAIR>
+template <int SHAPE>
 static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cudaStream_t s) {
+  constexpr bool PAIR = SHAPE == kNsPair;
   static int units_of[kMaxDevices] = {};
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   int& most = units_of[dev];
   if (most == 0) {
     cudaError_t e = cudaFuncSetAttribute(
-        ns_iterate_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmemBytes);
+        ns_iterate_kernel<SHAPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, ns_smem_bytes(SHAPE));
     if (e != cudaSuccess) return e;
     int n = sms;
     if (PAIR) {
@@ -26,10 +27,10 @@ static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cud
       attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
       cfg.blockDim = dim3(kNsThreads, 1, 1);
-      cfg.dynamicSmemBytes = kNsSmemBytes;
+      cfg.dynamicSmemBytes = ns_smem_bytes(SHAPE);
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n, ns_iterate_kernel<PAIR>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, ns_iterate_kernel<SHAPE>, &cfg);
       if (e != cudaSuccess) return e;
       if (n > sms / 2) n = sms / 2;
     }
@@ -41,13 +42,17 @@ static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cud
                                                                             : a.apply_tiles) *
                          a.batch;
   const int units = static_cast<int>(wide < most ? wide : most);
-  return launch_kernel(ns_iterate_kernel<PAIR>, dim3(static_cast<unsigned>(PAIR ? 2 * units : units)),
-                       dim3(kNsThreads), kNsSmemBytes, s, PAIR ? 2 : 1, false, m, a);
+  return launch_kernel(ns_iterate_kernel<SHAPE>, dim3(static_cast<unsigned>(PAIR ? 2 * units : units)),
+                       dim3(kNsThreads), ns_smem_bytes(SHAPE), s, PAIR ? 2 : 1, false, m, a);
 }
 
-cudaError_t launch_ns_iterate(bool pair, const NsMaps& m, const NsArgs& a, int sms,
+cudaError_t launch_ns_iterate(int shape, const NsMaps& m, const NsArgs& a, int sms,
                               cudaStream_t s) {
-  return pair ? launch_ns_impl<true>(m, a, sms, s) : launch_ns_impl<false>(m, a, sms, s);
+  switch (shape) {
+    case kNsPair: return launch_ns_impl<kNsPair>(m, a, sms, s);
+    case kNsSingle: return launch_ns_impl<kNsSingle>(m, a, sms, s);
+    default: return launch_ns_impl<kNsNarrow>(m, a, sms, s);
+  }
 }
 
 }  // namespace lmoe

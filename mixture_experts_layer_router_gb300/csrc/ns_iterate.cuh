@@ -46,9 +46,15 @@
 // always proceed. No buffer is overwritten early: a phase's inputs were read by
 // phases that its own predecessor has waited for.
 //
-// Tiles: PAIR = true: 256 x 256 on two SMs (cta_group::2, each CTA holds 128
-// rows of A and 128 of B); PAIR = false: 128 x 128 on one SM, for products
-// with few tiles. Either way a CTA takes in 16 KB + 16 KB a k-block.
+// Tiles (NsShape):
+//   pair    256 x 256 on two SMs (cta_group::2, each CTA holds 128 rows of A and
+//           128 of B): half the operand bytes of the others per product, for
+//           products that fill the GPU
+//   single  128 x 128 on one SM, 32 KB a k-block as in a pair's CTA
+//   narrow  128 x 64 on one SM, for products with so few tiles that latency
+//           decides: 24 KB a k-block (an SM takes in about 64 bytes a clock,
+//           which is what the mainloops of single tiles are bound by) and half
+//           as many results to store
 //
 //   warp 0      TMA producer (one lane), takes and publishes the tiles
 //   warp 1      TMEM allocator, MMA issuer (one lane; pair: the leader's)
@@ -64,14 +70,24 @@ namespace lmoe {
 enum NsPhase : int { kNsGram = 0, kNsPoly = 1, kNsApply = 2 };
 enum NsOut : int { kNsOutBf16 = 0, kNsOutWeightBf16 = 1, kNsOutWeightF32 = 2 };
 
+enum NsShape : int { kNsNarrow = 0, kNsSingle = 1, kNsPair = 2 };
+
 constexpr int kNsMaxSteps = 32;
 constexpr int kNsBK = 64;
-constexpr int kNsStages = 4;
 constexpr int kNsTileBytes = 128 * kNsBK * 2;  // 16 KB: 128 rows of one operand
-constexpr int kNsStageBytes = 2 * kNsTileBytes;
+__host__ __device__ constexpr int ns_bm(int shape) { return shape == kNsPair ? 256 : 128; }
+__host__ __device__ constexpr int ns_bn(int shape) {
+  return shape == kNsPair ? 256 : shape == kNsSingle ? 128 : 64;
+}
+__host__ __device__ constexpr int ns_stages(int shape) { return shape == kNsNarrow ? 7 : 4; }
+__host__ __device__ constexpr int ns_stage_bytes(int shape) {
+  return shape == kNsNarrow ? kNsTileBytes * 3 / 2 : kNsTileBytes * 2;
+}
+// epilogue slots of a warp: a narrow tile has one chunk a warp
+__host__ __device__ constexpr int ns_slots(int shape) { return shape == kNsNarrow ? 1 : 2; }
 constexpr int kNsEpiWarps = 8;
 constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;
-// Epilogue slots, two a warp: a 32 x 32 chunk of X in fp32 (128-byte rows, the
+// An epilogue slot: a 32 x 32 chunk of X in fp32 (128-byte rows, the
 // 128-byte swizzle), brought in by TMA ahead of the accumulators, changed in
 // place and stored by TMA, and the chunk's next fp16 copy (64-byte rows, 64-byte
 // swizzle). poly keeps A' and gram and poly their result and its mirror image in
@@ -79,14 +95,18 @@ constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;
 // of 8 neighbouring rows into different banks.
 constexpr int kNsX = 32 * 128;
 constexpr int kNsH = 32 * 64;
-constexpr int kNsWarpBytes = 2 * kNsX + 2 * kNsH;
 constexpr int kNsCoefBytes = kNsEpiWarps * 32 * 4;
 constexpr int kNsRing = 4;  // published tiles
 constexpr int kNsLooks = 64;
-constexpr int kNsBarrierBytes = 8 * (2 * kNsStages + 2 + 2 + 1 + 2 * kNsRing + 2 * kNsEpiWarps);
-constexpr int kNsSmemBytes = 1024 + kNsStages * kNsStageBytes + kNsEpiWarps * kNsWarpBytes +
-                             kNsCoefBytes + kNsBarrierBytes + 4 * kNsRing + 16;
-static_assert(kNsSmemBytes <= 232448, "Newton-Schulz shared memory");
+__host__ __device__ constexpr int ns_smem_bytes(int shape) {
+  return 1024 + ns_stages(shape) * ns_stage_bytes(shape) +
+         kNsEpiWarps * ns_slots(shape) * (kNsX + kNsH) + kNsCoefBytes +
+         8 * (2 * ns_stages(shape) + 2 + 2 + 1 + 2 * kNsRing + kNsEpiWarps * ns_slots(shape)) +
+         4 * kNsRing + 16;
+}
+static_assert(ns_smem_bytes(kNsNarrow) <= 232448 && ns_smem_bytes(kNsSingle) <= 232448 &&
+                  ns_smem_bytes(kNsPair) <= 232448,
+              "Newton-Schulz shared memory");
 constexpr int kNsEarly = 2;  // steps in which P keeps its diagonal
 
 // Factors of one step; s_x, s_a, s_p: the scales of the fp16 X, A', P'.
@@ -187,7 +207,7 @@ struct NsTile {
   bool mirror;     // symmetric result, tile below the diagonal
 };
 
-template <int BT>
+template <int SHAPE>
 __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
   NsTile c;
   const int per_step = 2 * a.sym_tiles + a.apply_tiles;  // of one matrix
@@ -212,31 +232,34 @@ __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
   const int mi = r / tiles;
   c.b = first + mi;
   const int local = r - mi * tiles;
+  constexpr int BM = ns_bm(SHAPE), BN = ns_bn(SHAPE);
+  constexpr int R = BM / BN;  // tiles across a square of the diagonal
   int i, j;
   if (c.phase != kNsApply) {
-    // row i of the lower triangle starts at i (i + 1) / 2
-    i = static_cast<int>((sqrtf(8.0f * static_cast<float>(local) + 1.0f) - 1.0f) * 0.5f);
-    while (i > 0 && i * (i + 1) / 2 > local) --i;
-    while ((i + 1) * (i + 2) / 2 <= local) ++i;
-    j = local - i * (i + 1) / 2;
-    c.mirror = i != j;
+    // row i of the lower triangle has R (i + 1) tiles and starts at R i (i + 1) / 2
+    const float x = static_cast<float>(local) * (8.0f / R) + 1.0f;
+    i = static_cast<int>((sqrtf(x) - 1.0f) * 0.5f);
+    while (i > 0 && R * (i * (i + 1) / 2) > local) --i;
+    while (R * ((i + 1) * (i + 2) / 2) <= local) ++i;
+    j = local - R * (i * (i + 1) / 2);
+    c.mirror = j < R * i;
   } else {
     j = local / a.m_tiles;
     i = local - j * a.m_tiles;
     c.mirror = false;
   }
-  c.row0 = i * BT;
-  c.col0 = j * BT;
+  c.row0 = i * BM;
+  c.col0 = j * BN;
   return c;
 }
 
-// One operand's 128 x 64 tile: rows / columns mn0.. of matrix b, from k0 on.
-template <bool PAIR>
+// One operand's ROWS x 64 tile: rows / columns mn0.. of matrix b, from k0 on.
+template <bool PAIR, int ROWS>
 __device__ __forceinline__ void ns_load(const CUtensorMap* map, bool mn, uint64_t* bar,
                                         uint32_t bar_cluster, uint8_t* dst, int mn0, int k0, int b,
                                         uint64_t pol) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < ROWS / 64; ++h) {
     const int c0 = mn ? mn0 + 64 * h : k0;
     const int c1 = mn ? k0 : mn0 + 64 * h;
     uint8_t* d = dst + h * (kNsTileBytes / 2);
@@ -478,15 +501,20 @@ __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-template <bool PAIR>
+template <int SHAPE>
 __global__ void __launch_bounds__(kNsThreads, 1)
     ns_iterate_kernel(const __grid_constant__ NsMaps tm, const __grid_constant__ NsArgs a) {
+  constexpr bool PAIR = SHAPE == kNsPair;
+  constexpr int kNsStages = ns_stages(SHAPE);
+  constexpr int kNsStageBytes = ns_stage_bytes(SHAPE);
+  constexpr int kSlots = ns_slots(SHAPE);
+  constexpr int kWarpBytes = kSlots * (kNsX + kNsH);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* tiles = smem;
   uint8_t* slots = smem + kNsStages * kNsStageBytes;
-  float* coefs = reinterpret_cast<float*>(slots + kNsEpiWarps * kNsWarpBytes);
+  float* coefs = reinterpret_cast<float*>(slots + kNsEpiWarps * kWarpBytes);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(coefs + kNsEpiWarps * 32);
   uint64_t* empty_bar = full_bar + kNsStages;
   uint64_t* tfull_bar = empty_bar + kNsStages;
@@ -494,13 +522,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   uint64_t* done_bar = tempty_bar + 2;
   uint64_t* tr_full = done_bar + 1;         // [kNsRing]
   uint64_t* tr_empty = tr_full + kNsRing;   // [kNsRing], pair: the leader's is used
-  uint64_t* slot_bar = tr_empty + kNsRing;  // [kNsEpiWarps][2]
-  int* tile_ring = reinterpret_cast<int*>(slot_bar + 2 * kNsEpiWarps);
+  uint64_t* slot_bar = tr_empty + kNsRing;  // [kNsEpiWarps][kSlots]
+  int* tile_ring = reinterpret_cast<int*>(slot_bar + kSlots * kNsEpiWarps);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_ring + kNsRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  constexpr int kBT = PAIR ? 256 : 128;  // tile rows and columns
-  constexpr int kTmem = 2 * kBT;         // two accumulators of kBT columns
+  constexpr int kBM = ns_bm(SHAPE), kBN = ns_bn(SHAPE);  // tile
+  constexpr int kBRows = PAIR ? 128 : kBN;               // of B in this CTA
+  constexpr int kTmem = 2 * kBN;                         // two accumulators
   // readers of a published tile: the MMA issuer, the epilogue warps and, in a
   // pair, the other CTA's producer and epilogue warps
   constexpr int kReaders = PAIR ? 2 + 2 * kNsEpiWarps : 1 + kNsEpiWarps;
@@ -576,7 +605,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       mbar_init(&tr_full[i], 1);
       mbar_init(&tr_empty[i], kReaders);
     }
-    for (int i = 0; i < 2 * kNsEpiWarps; ++i) mbar_init(&slot_bar[i], 1);
+    for (int i = 0; i < kSlots * kNsEpiWarps; ++i) mbar_init(&slot_bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -646,7 +675,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           t = read_tile(slot, slot_ph);
         }
         if (t < 0) break;
-        const NsTile c = ns_decode<kBT>(t, a);
+        const NsTile c = ns_decode<SHAPE>(t, a);
         const CUtensorMap* mx = &tm.x[c.step & 1];
         const CUtensorMap* ma = c.phase == kNsPoly ? &tm.gram : mx;
         const CUtensorMap* mb = ma;
@@ -676,8 +705,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           const uint32_t fb = PAIR ? mapa_shared(smem_addr(&full_bar[stage]), 0) : 0u;
           if (leader)
             mbar_arrive_expect_tx(&full_bar[stage], (PAIR ? 2u : 1u) * kNsStageBytes);
-          ns_load<PAIR>(ma, amn, &full_bar[stage], fb, sa, arow, kb * kNsBK, c.b, pol);
-          ns_load<PAIR>(mb, bmn, &full_bar[stage], fb, sa + kNsTileBytes, brow, kb * kNsBK, c.b,
+          ns_load<PAIR, 128>(ma, amn, &full_bar[stage], fb, sa, arow, kb * kNsBK, c.b, pol);
+          ns_load<PAIR, kBRows>(mb, bmn, &full_bar[stage], fb, sa + kNsTileBytes, brow, kb * kNsBK, c.b,
                         pol);
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -704,17 +733,17 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       while (ok) {
         const int t = read_tile(slot, slot_ph);
         if (t < 0) break;
-        const NsTile c = ns_decode<kBT>(t, a);
+        const NsTile c = ns_decode<SHAPE>(t, a);
         const bool amn = c.phase == kNsGram && a.tall != 0;
         const bool bmn = c.phase == kNsGram ? amn : c.phase == kNsApply && a.tall == 0;
-        const uint32_t idesc = instr_desc_f16(kBT, kBT, amn, bmn);
+        const uint32_t idesc = instr_desc_f16(kBM, kBN, amn, bmn);
         // 16 elements of K: 32 bytes along a K-major row, 16 rows of 128 bytes otherwise
         const uint64_t step_a = amn ? 128ull : 2ull;
         const uint64_t step_b = bmn ? 128ull : 2ull;
         const int kbs = c.phase == kNsGram ? a.k_gram : a.k_side;
         if (!wait1(&tempty_bar[acc], acc_phase ^ 1u)) break;
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBT);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
         for (int kb = 0; kb < kbs; ++kb) {
           if (!wait1(&full_bar[stage], phase)) {
             ok = false;
@@ -752,9 +781,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   } else {
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
-    uint8_t* my_slots = slots + (warp - 2) * kNsWarpBytes;
+    uint8_t* my_slots = slots + (warp - 2) * kWarpBytes;
     float* coef = coefs + (warp - 2) * 32;
-    uint64_t* my_bars = slot_bar + 2 * (warp - 2);
+    uint64_t* my_bars = slot_bar + kSlots * (warp - 2);
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_addr(&tempty_bar[0]), 0) : 0u;
     const uint64_t pol = policy_evict_normal();
     int acc = 0;
@@ -768,7 +797,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       if (lane == 0) t = read_tile(slot, slot_ph);
       t = __shfl_sync(0xffffffffu, t, 0);
       if (t < 0) break;
-      const NsTile c = ns_decode<kBT>(t, a);
+      const NsTile c = ns_decode<SHAPE>(t, a);
       const NsStep& f = a.step[c.step];
       const bool sym = c.phase != kNsApply;
       const bool poly = c.phase == kNsPoly;
@@ -778,14 +807,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       const int col0 = c.col0 + half * 32;
       // this warp's chunks: columns col0, col0 + 64, ...
       int chunks = 0;
-      if (row < M && col0 < N) chunks = min(kBT / 64, (N - col0 + 63) / 64);
-      // lane 0: bring chunk i into slot i & 1
+      if (row < M && col0 < N) chunks = min(kBN / 64, (N - col0 + 63) / 64);
+      // lane 0: bring chunk i into slot i % kSlots
       auto load_chunk = [&](int i) {
-        uint64_t* bar = &my_bars[i & 1];
+        uint64_t* bar = &my_bars[i % kSlots];
         mbar_arrive_expect_tx(bar, poly ? kNsH : kNsX);
-        tma_load_3d(poly ? &tm.chunk_gram : &tm.chunk_x, bar, my_slots + (i & 1) * kNsX,
-                    col0 + 64 * i, row, c.b, pol);
-        in_flight |= 1u << (i & 1);
+        tma_load_3d(poly ? &tm.chunk_gram : &tm.chunk_x, bar,
+                    my_slots + (i % kSlots) * kNsX, col0 + 64 * i, row, c.b, pol);
+        in_flight |= 1u << (i % kSlots);
       };
       // the old values and the diagonals are read while the MMAs run (the slots
       // are free: the last tile's stores have been waited for). by_row: d of the
@@ -805,7 +834,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           if (ok) {
             fence_proxy_async_global();
             load_chunk(0);
-            if (chunks > 1) load_chunk(1);
+            if (kSlots > 1 && chunks > 1) load_chunk(1);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -817,12 +846,13 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       if (!wait32(&tfull_bar[acc], acc_phase)) break;
       tc_fence_after_sync();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                             static_cast<uint32_t>(acc * kBT + half * 32);
+                             static_cast<uint32_t>(acc * kBN + half * 32);
       bool ok = true;
       for (int i = 0; i < chunks; ++i) {
         const int col = col0 + 64 * i;
-        uint8_t* sx = my_slots + (i & 1) * kNsX;
-        uint8_t* sh = my_slots + 2 * kNsX + (i & 1) * kNsH;
+        const int sl = i % kSlots;
+        uint8_t* sx = my_slots + sl * kNsX;
+        uint8_t* sh = my_slots + kSlots * kNsX + sl * kNsH;
         uint32_t v[32];
         tmem_ld_32cols(tbase + static_cast<uint32_t>(64 * i), v);
         if (cols_differ) {
@@ -839,12 +869,12 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           }
         }
         if (c.phase != kNsGram) {
-          if (!wait32(&my_bars[i & 1], (bar_ph >> (i & 1)) & 1u)) {
+          if (!wait32(&my_bars[sl], (bar_ph >> sl) & 1u)) {
             ok = false;
             break;
           }
-          bar_ph ^= 1u << (i & 1);
-          if (lane == 0) in_flight &= ~(1u << (i & 1));
+          bar_ph ^= 1u << sl;
+          if (lane == 0) in_flight &= ~(1u << sl);
         }
         __syncwarp();
         tmem_ld_wait();
@@ -911,7 +941,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     }
     if (lane == 0) {
       // after a wait that gave up: what is still in flight
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < kSlots; ++s)
         if (in_flight & (1u << s)) wait_drain(&my_bars[s], (bar_ph >> s) & 1u);
       bulk_wait_all();
     }

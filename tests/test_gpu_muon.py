@@ -62,7 +62,7 @@ SIZES = [(1, 1, 1), (1, 1, 200), (1, 200, 1), (2, 7, 5), (1, 64, 64), (1, 128, 1
          (1, 256, 256), (1, 130, 4100)]
 
 
-@pytest.mark.parametrize("pairs", [0, 1, 2])
+@pytest.mark.parametrize("pairs", [0, 1, 2, 3])
 @pytest.mark.parametrize("batch,rows,cols", SIZES)
 def test_orthogonalize(batch, rows, cols, pairs):
     gh.lib()
@@ -262,7 +262,7 @@ def test_refusals():
         assert step(**bad) == capi.ERR_INVALID_ARG, bad
     assert step(w=w.data_ptr() + 4) == step(momentum=mo.data_ptr() + 8) == capi.ERR_UNSUPPORTED
     assert lib.latentmoe_muon_step(hd, None, None) == capi.ERR_INVALID_ARG
-    for mode in (-1, 3):
+    for mode in (-1, 4):
         assert lib.latentmoe_muon_set_sm_pairs(hd, mode) == capi.ERR_INVALID_ARG
     torch.cuda.synchronize()
     for bad in (g[0], g.half(), g.cpu(), g.mT, g[:, :, :40]):
