@@ -418,3 +418,30 @@ def test_refusals():
         args.update(bad)
         with pytest.raises(ValueError):
             h.router_backward(**args)
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 logits: uniform rows but for the last three, whose part of the
+    sums and gradients is known by itself."""
+    T, E, k = 2 ** 22 + 3, 512, 1
+    h = layer(E, k, T)
+    logits = torch.zeros((T, E), device="cuda")
+    tail, _, _, _ = inputs(3, E, k, 3, scale=2.0)
+    logits[-3:] = tail
+    idx = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    idx[-3:, 0] = torch.tensor([E - 1, 5, E - 1], device="cuda")
+    got = h.balance_loss(logits, idx, balance_coef=1.0, z_coef=0.5)
+    assert int(got["tokens"]) == T
+    assert got["counts"][0, [0, 5, E - 1]].tolist() == [T - 3, 1, 2]
+    p = torch.softmax(tail.double(), 1)
+    want = torch.full((E,), (T - 3) / E, dtype=torch.float64, device="cuda") + p.sum(0)
+    # a lane adds up to 2000 equal terms here: 2000 roundings
+    assert rel(got["prob_sum"][0], want) <= 2000 * 2.0 ** -24
+    d = h.router_backward(logits, idx, got["counts"], got["tokens"], balance_coef=1.0, z_coef=0.5)
+    w = got["counts"][0].double() * E / (k * float(T) ** 2)
+    lse = torch.logsumexp(tail.double(), 1, keepdim=True)
+    q = 2 * 0.5 / T
+    dot = (p * w).sum(1, keepdim=True)
+    ref = p * (w - dot + q * lse)
+    size = p * (w + dot + q * lse.abs())
+    assert bool(((d[-3:].double() - ref).abs() <= G_TOL * size + 1e-30).all())

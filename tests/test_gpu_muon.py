@@ -273,3 +273,20 @@ def test_refusals():
     with pytest.raises(ValueError):
         m.step(w, g, mo.bfloat16(), lr=0.1)
     assert m.status() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """A stack of more than 2^31 elements: its first and last matrices are right,
+    the zeros between stay zero."""
+    gh.lib()
+    batch, side = 1100, 1400
+    assert batch * side * side > 2 ** 31
+    m = capi.Muon(side, side, batch=batch)
+    g = torch.zeros((batch, side, side), dtype=torch.bfloat16, device="cuda")
+    for b in (0, batch - 1):
+        g[b] = rand((side, side), 50 + b).to(torch.bfloat16)
+    o = m.orthogonalize(g)
+    assert m.status() == 0
+    for b in (0, batch - 1):
+        assert rel(o[b], newton_schulz(g[b])) <= TOL
+    assert not bool(o[1:batch - 1].any())
