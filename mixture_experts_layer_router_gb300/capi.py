@@ -365,29 +365,22 @@ class LatentMoE:
         """The router's balance loss of logits [T, E] fp32 and choices idx
         [T, k] int32: {"loss": [total, balance, z], "counts" [S, E] int32,
         "prob_sum" [S, E], "z_sum" [S], "tokens" [S] int32} over S = T /
-        seq_len sequences (0: one). The five are views of one allocation."""
+        seq_len sequences (0: one)."""
         import torch
         T, E = logits.shape[0], self.dims.num_experts
         ld = self._rows(logits, "logits", T)
         self._per_slot(idx, "idx", T, torch.int32)
         S = self._sequences(T, seq_len)
-        n = S * E
-        # counts, tokens, prob_sum, z_sum, loss
-        flts = torch.empty((2 * (n + S) + 3,), dtype=torch.float32, device=logits.device)
-        p = flts.data_ptr()
-        at = (0, n, n + S, 2 * n + S, 2 * (n + S))
-        st = latentmoe_balance_stats(p, p + 4 * at[2], p + 4 * at[3], p + 4 * at[1])
+        # new_empty of the inputs: the cheapest way to five small outputs
+        loss, prob, z = logits.new_empty(3), logits.new_empty((S, E)), logits.new_empty(S)
+        counts, tokens = idx.new_empty((S, E)), idx.new_empty(S)
+        st = latentmoe_balance_stats(counts.data_ptr(), prob.data_ptr(), z.data_ptr(),
+                                     tokens.data_ptr())
         check(load().latentmoe_balance_loss(
             self.handle, logits.data_ptr(), ld, idx.data_ptr(), self._valid(valid, T), T, seq_len,
-            balance_coef, z_coef, ctypes.byref(st), p + 4 * at[4], _stream(stream)),
+            balance_coef, z_coef, ctypes.byref(st), loss.data_ptr(), _stream(stream)),
             "latentmoe_balance_loss", self.handle)
-        ints = flts.view(torch.int32)
-        rows, one = (S, E), (E, 1)
-        return {"loss": flts.as_strided((3,), (1,), at[4]),
-                "counts": ints.as_strided(rows, one, 0),
-                "prob_sum": flts.as_strided(rows, one, at[2]),
-                "z_sum": flts.as_strided((S,), (1,), at[3]),
-                "tokens": ints.as_strided((S,), (1,), at[1])}
+        return {"loss": loss, "counts": counts, "prob_sum": prob, "z_sum": z, "tokens": tokens}
 
     def balance_loss_from_stats(self, stats, balance_coef: float = 1.0, z_coef: float = 0.0,
                                 stream=None):
@@ -429,7 +422,7 @@ class LatentMoE:
             _need(d_loss.is_cuda and d_loss.dtype == torch.float32 and d_loss.numel() == 1,
                   "d_loss must be one float32 on the GPU")
         if out is None:
-            out = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+            out = logits.new_empty((T, E))
         check(load().latentmoe_router_backward(
             self.handle, logits.data_ptr(), ld, _ptr(idx), _ptr(d_gates), self._valid(valid, T),
             counts.data_ptr(), tokens.data_ptr(), T, seq_len, balance_coef, z_coef, _ptr(d_loss),
