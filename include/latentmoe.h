@@ -14,6 +14,12 @@
  *   c[t] = sum_j g[t,j] H[pos[t,j]]          gate-weighted combine, fp32, j order
  *   y = c W_up^T (+ (SiLU(x W_gs^T) * (x W_us^T)) W_ds^T)   up-projection + shared
  *
+ * Beside it, for training the router and the layer's matrices: the router's
+ * balance loss with per-expert counts (latentmoe_balance_loss), the gradient
+ * of that loss and of the gates with respect to the logits
+ * (latentmoe_router_backward), and orthogonalised matrix updates
+ * (latentmoe_muon_*).
+ *
  * Conventions for every entry point:
  * - Return 0 (LATENTMOE_OK) on success, a negative LATENTMOE_ERR_* otherwise.
  *   No C++ exception crosses the ABI and no kernel traps.

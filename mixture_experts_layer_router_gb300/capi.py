@@ -1,7 +1,8 @@
 """ctypes binding of liblatentmoe.so (include/latentmoe.h), same names.
 
-Argument marshalling only: every step of the layer runs in the library's
-CUDA kernels. PyTorch provides device memory (``tensor.data_ptr()``) and
+Argument marshalling only: every step of the layer, and of the training
+operators (balance loss, router backward, Muon), runs in the library's CUDA
+kernels. PyTorch provides device memory (``tensor.data_ptr()``) and
 streams (``torch.cuda.current_stream().cuda_stream``). There is no fallback:
 ``load()`` raises if the library is missing or cannot be loaded.
 """
