@@ -195,19 +195,21 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
 
 // True in every thread of the CTA that arrives last of `n` at *ticket; the
 // others' global writes before their arrival are visible to it. The last one
-// leaves the ticket at zero.
+// leaves the ticket at zero. One thread's release and acquire stand for the CTA:
+// the barriers around it carry the other threads' writes and reads.
 __device__ __forceinline__ bool arrive_last(unsigned* ticket, unsigned n, int* flag) {
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const unsigned old = atomicAdd(ticket, 1u);
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(old)
+                 : "l"(ticket)
+                 : "memory");
     *flag = old == n - 1;
     if (old == n - 1) *ticket = 0;
   }
   __syncthreads();
-  const bool last = *flag != 0;
-  if (last) __threadfence();
-  return last;
+  return *flag != 0;
 }
 
 __device__ __forceinline__ void store_loss(float* loss, float balance, float z, float bc,
