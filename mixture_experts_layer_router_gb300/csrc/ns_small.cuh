@@ -8,7 +8,7 @@
 // where the same bytes serve as K-major operand of the gram product and as
 // MN-major operand of the apply product. A step:
 //   gram   partial A = X_r X_r^T (M = N = 128, K = W), to shared memory in fp32;
-//          each CTA adds its share of the rows over the cluster (in rank order)
+//          each CTA adds its share of the rows over the cluster (in a fixed order)
 //          through distributed shared memory and hands the fp16 A' and the fp32
 //          diagonal d to all CTAs
 //   poly   P = b A + c A A, by every CTA for itself (K = m)
@@ -80,15 +80,25 @@ __device__ __forceinline__ int op_at(int row, int k8) {
   return (k8 >> 3) * 16384 + row * 128 + (((k8 & 7) ^ (row & 7)) << 4);
 }
 
-// 32 elements X[i, j0 ..] of a [m, n] matrix stored as it is (wide) or
-// transposed, zeros outside.
+// A warp's 32 x 32 chunk X[i0 .., j0 ..] of a [m, n] matrix that is stored as it is
+// (wide) or transposed (tall), thread = row; zeros outside. Whole vectors where
+// rows start on them; transposed, the lanes of a column are neighbours in memory;
+// else row by row through `turn` (32 x 33 floats of this warp).
 template <class T>
-__device__ __forceinline__ void small_load(const T* p, const NsSmallArgs& a, int i, int j0,
-                                           float (&v)[32]) {
+__device__ __forceinline__ void small_load(const T* p, const NsSmallArgs& a, int i0, int j0,
+                                           float* turn, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const int i = i0 + lane;
+  if (a.tall) {
+    const T* at = p + static_cast<long long>(j0) * a.cols + i;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-  if (i >= a.m) return;
-  if (!a.tall && (a.cols & 7) == 0 && j0 + 32 <= a.n) {
+    for (int k = 0; k < 32; ++k)
+      v[k] = i < a.m && j0 + k < a.n ? static_cast<float>(at[static_cast<long long>(k) * a.cols])
+                                     : 0.0f;
+  } else if ((a.cols & 7) == 0 && j0 + 32 <= a.n) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+    if (i >= a.m) return;
     const T* row = p + static_cast<long long>(i) * a.cols + j0;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -111,22 +121,39 @@ __device__ __forceinline__ void small_load(const T* p, const NsSmallArgs& a, int
         }
       }
     }
-    return;
-  }
-  const long long step = a.tall ? a.cols : 1;
-  const T* at = p + (a.tall ? static_cast<long long>(j0) * a.cols + i
-                            : static_cast<long long>(i) * a.cols + j0);
+  } else {
+    const T* at = p + static_cast<long long>(i0) * a.cols + j0 + lane;
 #pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (j0 + k < a.n) v[k] = static_cast<float>(at[k * step]);
+    for (int k = 0; k < 32; ++k)
+      v[k] = i0 + k < a.m && j0 + lane < a.n
+                 ? static_cast<float>(at[static_cast<long long>(k) * a.cols])
+                 : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) turn[k * 33 + lane] = v[k];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = turn[lane * 33 + k];
+    __syncwarp();
+  }
 }
 
 // The same places written: T = float or bf16.
 template <class T>
-__device__ __forceinline__ void small_store(T* p, const NsSmallArgs& a, int i, int j0,
+__device__ __forceinline__ void small_store(T* p, const NsSmallArgs& a, int i0, int j0, float* turn,
                                             const float (&v)[32]) {
-  if (i >= a.m) return;
-  if (!a.tall && (a.cols & 7) == 0 && j0 + 32 <= a.n) {
+  const int lane = threadIdx.x & 31;
+  const int i = i0 + lane;
+  auto put = [](T* to, float x) {
+    if constexpr (sizeof(T) == 4) *to = x;
+    else *to = __float2bfloat16_rn(x);
+  };
+  if (a.tall) {
+    T* at = p + static_cast<long long>(j0) * a.cols + i;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (i < a.m && j0 + k < a.n) put(at + static_cast<long long>(k) * a.cols, v[k]);
+  } else if ((a.cols & 7) == 0 && j0 + 32 <= a.n) {
+    if (i >= a.m) return;
     T* row = p + static_cast<long long>(i) * a.cols + j0;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -141,17 +168,16 @@ __device__ __forceinline__ void small_store(T* p, const NsSmallArgs& a, int i, i
                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
                        pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
     }
-    return;
-  }
-  const long long step = a.tall ? a.cols : 1;
-  T* at = p + (a.tall ? static_cast<long long>(j0) * a.cols + i
-                      : static_cast<long long>(i) * a.cols + j0);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (j0 + k < a.n) {
-      if constexpr (sizeof(T) == 4) at[k * step] = v[k];
-      else at[k * step] = __float2bfloat16_rn(v[k]);
-    }
+    for (int k = 0; k < 32; ++k) turn[lane * 33 + k] = v[k];
+    __syncwarp();
+    T* at = p + static_cast<long long>(i0) * a.cols + j0 + lane;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (i0 + k < a.m && j0 + lane < a.n)
+        put(at + static_cast<long long>(k) * a.cols, turn[k * 33 + lane]);
+    __syncwarp();
   }
 }
 
@@ -180,6 +206,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int col0 = rank * a.width;  // of X
   const int chunks = a.width / 32;
   const int mk = (a.m + 15) & ~15;  // rows (and k) that hold something
+  float* turn = reinterpret_cast<float*>(part) + warp * (32 * 33);  // while part is idle
 
   if (threadIdx.x == 0) {
     mbar_init(bar, 1);
@@ -227,17 +254,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   for (int ch = half; ch < chunks; ch += 2) {
     const int j0 = col0 + ch * 32;
     float v[32];
-    if (a.g_f32) small_load(static_cast<const float*>(a.g) + base, a, row, j0, v);
-    else small_load(static_cast<const __nv_bfloat16*>(a.g) + base, a, row, j0, v);
+    if (a.g_f32) small_load(static_cast<const float*>(a.g) + base, a, quarter * 32, j0, turn, v);
+    else small_load(static_cast<const __nv_bfloat16*>(a.g) + base, a, quarter * 32, j0, turn, v);
     if (a.momentum != nullptr) {
       float mo[32];
-      small_load(a.momentum + base, a, row, j0, mo);
+      small_load(a.momentum + base, a, quarter * 32, j0, turn, mo);
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         mo[k] = __fadd_rn(__fmul_rn(a.mu, mo[k]), v[k]);
         v[k] = a.nesterov ? __fadd_rn(v[k], __fmul_rn(a.mu, mo[k])) : mo[k];
       }
-      small_store(a.momentum + base, a, row, j0, mo);
+      small_store(a.momentum + base, a, quarter * 32, j0, turn, mo);
     }
     uint32_t r[32];
 #pragma unroll
@@ -297,67 +324,99 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       tc_commit(bar);
     }
     wait_mma();
-    if (quarter * 32 < mk) {
-      for (int ch = half; ch * 32 < mk; ch += 2) {
-        uint32_t r[32];
-        tmem_ld_32cols(t_acc + static_cast<uint32_t>(32 * ch), r);
-        tmem_ld_wait();
+    if (a.ctas == 1) {
+      // the accumulators are the whole A
+      if (quarter * 32 < mk) {
+        for (int ch = half; ch * 32 < mk; ch += 2) {
+          uint32_t r[32];
+          tmem_ld_32cols(t_acc + static_cast<uint32_t>(32 * ch), r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(part + row * 512 + (((8 * ch + q) ^ (row & 7)) << 4)) =
-              make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-      }
-    }
-    tc_fence_before_sync();
-    cluster_sync();
-    {
-      // rows rank, rank + ctas, ... of the sum, 4 columns a thread
-      const int per_row = mk / 4;
-      const int items = ((mk - rank + a.ctas - 1) / a.ctas) * per_row;
-      const uint32_t part0 = smem_addr(part);
-      for (int it = threadIdx.x; it < items; it += kSmallThreads) {
-        const int r = rank + (it / per_row) * a.ctas;
-        const int q = it % per_row;
-        const uint32_t at = part0 + static_cast<uint32_t>(r * 512 + ((q ^ (r & 7)) << 4));
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int p0 = 0; p0 < a.ctas; p0 += 8) {
-          float4 w[8];
+          for (int q = 0; q < 4; ++q) {
+            float x[8];
 #pragma unroll
-          for (int p = 0; p < 8; ++p)
-            w[p] = p0 + p < a.ctas ? ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(p0 + p)))
-                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < 8; ++i) x[i] = f.gram_off * __uint_as_float(r[8 * q + i]);
+            *reinterpret_cast<uint4*>(aop + op_at(row, 4 * ch + q)) = float_to_half8(x);
+          }
+          if (ch == quarter) {
+            float acc = 0.0f;
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            v.x += w[p].x;
-            v.y += w[p].y;
-            v.z += w[p].z;
-            v.w += w[p].w;
+            for (int j = 0; j < 32; ++j) acc = lane == j ? __uint_as_float(r[j]) : acc;
+            diag[row] = f.gram_diag * acc;
+            *reinterpret_cast<__half*>(aop + op_at(row, row >> 3) + (row & 7) * 2) =
+                __float2half_rn(0.0f);
           }
         }
-        float x[4] = {v.x, v.y, v.z, v.w};
-        float d = 0.0f;
-        const bool has_d = r >= 4 * q && r < 4 * q + 4;
+      }
+    } else {
+      if (quarter * 32 < mk) {
+        for (int ch = half; ch * 32 < mk; ch += 2) {
+          uint32_t r[32];
+          tmem_ld_32cols(t_acc + static_cast<uint32_t>(32 * ch), r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (4 * q + i == r) d = x[i] * f.gram_diag;
-          x[i] = 4 * q + i == r ? 0.0f : x[i] * f.gram_off;
-        }
-        const __half2 h01 = __floats2half2_rn(x[0], x[1]), h23 = __floats2half2_rn(x[2], x[3]);
-        const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&h01),
-                                   *reinterpret_cast<const uint32_t*>(&h23));
-        const uint32_t to = smem_addr(aop) + static_cast<uint32_t>(op_at(r, q >> 1) + (q & 1) * 8);
-        const uint32_t dto = smem_addr(&diag[r]);
-        for (int p = 0; p < a.ctas; ++p) {
-          st_cluster_u2(mapa_shared(to, static_cast<uint32_t>(p)), h);
-          if (has_d) st_cluster_f32(mapa_shared(dto, static_cast<uint32_t>(p)), d);
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(part + row * 512 + (((8 * ch + q) ^ (row & 7)) << 4)) =
+                make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
         }
       }
+      tc_fence_before_sync();
+      cluster_sync();
+      {
+        // rows rank, rank + ctas, ... of the sum, 4 columns a thread
+        const int per_row = mk / 4;
+        const int items = ((mk - rank + a.ctas - 1) / a.ctas) * per_row;
+        const uint32_t part0 = smem_addr(part);
+        for (int it = threadIdx.x; it < items; it += kSmallThreads) {
+          const int r = rank + (it / per_row) * a.ctas;
+          const int q = it % per_row;
+          const uint32_t at = part0 + static_cast<uint32_t>(r * 512 + ((q ^ (r & 7)) << 4));
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int p0 = 0; p0 < a.ctas; p0 += 8) {
+            float4 w[8];
+            // in turn from this CTA on, so that not all ask the same one at a time
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              int from = rank + p0 + p;
+              if (from >= a.ctas) from -= a.ctas;
+              w[p] = p0 + p < a.ctas ? ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(from)))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              v.x += w[p].x;
+              v.y += w[p].y;
+              v.z += w[p].z;
+              v.w += w[p].w;
+            }
+          }
+          float x[4] = {v.x, v.y, v.z, v.w};
+          float d = 0.0f;
+          const bool has_d = r >= 4 * q && r < 4 * q + 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (4 * q + i == r) d = x[i] * f.gram_diag;
+            x[i] = 4 * q + i == r ? 0.0f : x[i] * f.gram_off;
+          }
+          const __half2 h01 = __floats2half2_rn(x[0], x[1]), h23 = __floats2half2_rn(x[2], x[3]);
+          const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&h01),
+                                     *reinterpret_cast<const uint32_t*>(&h23));
+          const uint32_t to = smem_addr(aop) + static_cast<uint32_t>(op_at(r, q >> 1) + (q & 1) * 8);
+          const uint32_t dto = smem_addr(&diag[r]);
+          for (int p = 0; p < a.ctas; ++p) {
+            int dst = rank + p;
+            if (dst >= a.ctas) dst -= a.ctas;
+            st_cluster_u2(mapa_shared(to, static_cast<uint32_t>(dst)), h);
+            if (has_d) st_cluster_f32(mapa_shared(dto, static_cast<uint32_t>(dst)), d);
+          }
+        }
+      }
+      // other CTAs' shared memory is written: ordered before their MMAs by this
+      // fence, the cluster barrier and their own fence
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+      cluster_sync();
     }
-    // other CTAs' shared memory is written: ordered before their MMAs by this
-    // fence, the cluster barrier and their own fence
-    asm volatile("fence.proxy.async;" ::: "memory");
-    __syncwarp();
-    cluster_sync();
     // ---- poly
     to_mma();
     if (threadIdx.x == 0) {
@@ -443,21 +502,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         } else {
           const int j0 = col0 + 32 * ch;
           if (a.out_mode == kNsOutBf16) {
-            small_store(static_cast<__nv_bfloat16*>(a.out) + base, a, row, j0, x);
+            small_store(static_cast<__nv_bfloat16*>(a.out) + base, a, quarter * 32, j0, turn, x);
           } else if (a.out_mode == kNsOutWeightBf16) {
             __nv_bfloat16* w = static_cast<__nv_bfloat16*>(a.out) + base;
             float old[32];
-            small_load(w, a, row, j0, old);
+            small_load(w, a, quarter * 32, j0, turn, old);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = fmaf(a.keep, old[j], -a.move * x[j]);
-            small_store(w, a, row, j0, x);
+            small_store(w, a, quarter * 32, j0, turn, x);
           } else {
             float* w = static_cast<float*>(a.out) + base;
             float old[32];
-            small_load(w, a, row, j0, old);
+            small_load(w, a, quarter * 32, j0, turn, old);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = fmaf(a.keep, old[j], -a.move * x[j]);
-            small_store(w, a, row, j0, x);
+            small_store(w, a, quarter * 32, j0, turn, x);
           }
         }
       }
