@@ -152,8 +152,9 @@ struct Tops {
     }
     big = __any_sync(0xffffffffu, far) != 0;
   }
-  __device__ __forceinline__ float exp(int u, float x) const {
-    return big ? pow2((x - max[u]) * kLog2E) : pow2(fmaf(x, kLog2E, -top[u]));
+  // exp(x - m), m the maximum of a row of the warp, rounded as in exp_row
+  __device__ __forceinline__ float exp_of(float m, float x) const {
+    return big ? pow2((x - m) * kLog2E) : pow2(fmaf(x, kLog2E, -(m * kLog2E)));
   }
   // x <- exp(x - max); the lane's part of the sum. A row of -inf alone sums to 0,
   // a NaN makes its row's sum NaN.
@@ -480,48 +481,68 @@ __global__ void __launch_bounds__(kBalThreads)
   if (threadIdx.x == 0) store_loss(loss, bs, zs, bc, zc);
 }
 
+// A warp's lanes over the choices of its batch of rows: `span` lanes (the power of
+// two from k on) a row, one choice each, so one round covers 32 / span rows.
+template <class R>
+struct Choices {
+  static constexpr int ROUNDS = R::BATCH > 2 ? R::BATCH / 2 : 1;  // k = 16
+  int span, rounds, sub, c;
+  __device__ __forceinline__ explicit Choices(int k) {
+    const int lane = threadIdx.x & 31;
+    const int shift = k > 1 ? 32 - __clz(k - 1) : 0;
+    span = 1 << shift;
+    rounds = ((R::BATCH << shift) + 31) >> 5;
+    sub = lane >> shift;
+    c = lane & (span - 1);
+  }
+  __device__ __forceinline__ int row(int round) const { return round * (32 / span) + sub; }
+  template <class Op>
+  __device__ __forceinline__ float reduce(float v, Op op) const {
+    for (int o = span >> 1; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+};
+
 // What the backward reads for one batch of rows: the logits and, for the
 // gates' part, the lane's choices, their gradients and their logits.
 template <class R, bool GATES>
 struct BackRows {
+  static constexpr int ROUNDS = GATES ? Choices<R>::ROUNDS : 1;
   float x[R::U][R::N];
-  bool in[R::U];
   int valid[R::U];
-  int id[GATES ? R::U : 1][R::J];
-  float dg[GATES ? R::U : 1][R::J], xi[GATES ? R::U : 1][R::J];
+  int id[ROUNDS];
+  float dg[ROUNDS], xi[ROUNDS];
   __device__ __forceinline__ void load(const RouterBackwardArgs& a, long long t0, int base, int r1,
-                                       int q, int sub) {
+                                       int q, int sub, const Choices<R>& ch) {
+    if constexpr (GATES) {
+#pragma unroll
+      for (int p = 0; p < ROUNDS; ++p) {
+        if (p >= ch.rounds) break;
+        const int row = ch.row(p);
+        const bool has = row < R::BATCH && base + row < r1 && ch.c < a.k;
+        const long long at = (t0 + base + row) * a.k + ch.c;
+        id[p] = has ? a.idx[at] : -1;
+        dg[p] = has ? a.d_gates[at] : 0.0f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < R::U; ++u) {
       const int r = base + u * R::ROWS + sub;
-      const long long t = t0 + r;
-      in[u] = r < r1;
-      if constexpr (GATES) {
-#pragma unroll
-        for (int j = 0; j < R::J; ++j) {
-          const int c = q + R::LANES * j;
-          const bool has = in[u] && c < a.k;
-          id[u][j] = has ? a.idx[t * a.k + c] : -1;
-          dg[u][j] = has ? a.d_gates[t * a.k + c] : 0.0f;
-        }
-      }
-      R::load(a.logits + (in[u] ? t : t0 + base) * a.ld, q, a.E, x[u]);
-      valid[u] = in[u] && a.valid != nullptr ? a.valid[t] : 1;
+      const bool in = r < r1;
+      R::load(a.logits + (t0 + (in ? r : base)) * a.ld, q, a.E, x[u]);
+      valid[u] = in && a.valid != nullptr ? a.valid[t0 + r] : 1;
     }
   }
   // after load: the choices' logits (ids outside [0, E): none)
   __device__ __forceinline__ void gather(const RouterBackwardArgs& a, long long t0, int base,
-                                         int sub) {
+                                         const Choices<R>& ch) {
     if constexpr (GATES) {
 #pragma unroll
-      for (int u = 0; u < R::U; ++u) {
-        const float* row = a.logits + (t0 + base + u * R::ROWS + sub) * a.ld;
-#pragma unroll
-        for (int j = 0; j < R::J; ++j) {
-          const bool has = static_cast<unsigned>(id[u][j]) < static_cast<unsigned>(a.E);
-          if (!has) id[u][j] = -1;
-          xi[u][j] = has ? row[id[u][j]] : -INFINITY;
-        }
+      for (int p = 0; p < ROUNDS; ++p) {
+        if (p >= ch.rounds) break;
+        const bool has = static_cast<unsigned>(id[p]) < static_cast<unsigned>(a.E);
+        if (!has) id[p] = -1;
+        xi[p] = has ? a.logits[(t0 + base + ch.row(p)) * a.ld + id[p]] : -INFINITY;
       }
     }
   }
@@ -532,21 +553,25 @@ struct BackRows {
 //   g_j = p[idx_j] / sum_i p[idx_i], i.e. a softmax over the chosen logits
 //   alone (evaluated as that: no quotient of underflowed probabilities):
 //                              sum_{j: idx_j = e} g_j (dg_j - D)
-// The lanes of a row own one choice each, put its term into the warp's shared
-// row (zero between rows) and every lane picks up its own columns there.
+// The choices of a batch's rows are spread over the whole warp (see Choices), put
+// their terms into the rows' shared copies (zero between batches), and every lane
+// of a row picks up its own columns there.
 template <class R, bool GATES>
 __global__ void __launch_bounds__(kBackThreads)
     router_backward_kernel(const RouterBackwardArgs a, int parts, int part_rows) {
-  extern __shared__ float sparse_all[];  // [warps][U][ROWS][WIDTH]
+  extern __shared__ float back_smem[];  // [warps][BATCH][WIDTH], [warps][BATCH][2]
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q = lane % R::LANES, sub = lane / R::LANES;
   const int E = a.E, k = a.k;
-  float* sparse = sparse_all + warp * (R::U * R::ROWS * R::WIDTH);
+  float* sparse = back_smem + warp * (R::BATCH * R::WIDTH);
+  float2* stat = reinterpret_cast<float2*>(back_smem + (kBackThreads / 32) * R::BATCH * R::WIDTH) +
+                 warp * R::BATCH;  // max and 1 / sum of a row, then the sum of its terms
   if (GATES) {
-    for (int i = lane; i < R::U * R::ROWS * R::WIDTH; i += 32) sparse[i] = 0.0f;
+    for (int i = lane; i < R::BATCH * R::WIDTH; i += 32) sparse[i] = 0.0f;
     __syncwarp();
   }
+  const Choices<R> ch(k);
   const int s = blockIdx.x / parts, part = blockIdx.x - s * parts;
   const int r0 = part * part_rows;
   const int r1 = min(a.seq_len, r0 + part_rows);
@@ -565,108 +590,115 @@ __global__ void __launch_bounds__(kBackThreads)
     wt[i] = c < E ? wc * static_cast<float>(a.counts[static_cast<long long>(s) * E + c]) : 0.0f;
   }
   constexpr int kStride = (kBackThreads / 32) * R::BATCH;
-  // with one choice a lane there are registers for a second batch: its rows are
-  // on their way while the first one's are worked on
-  constexpr bool kAhead = R::J == 1;
+  // where there are registers for a second batch its rows are on their way while
+  // the first one's are worked on
+  constexpr bool kAhead = R::BATCH <= 8;
   BackRows<R, GATES> cur;
   int base = r0 + warp * R::BATCH;
-  if (kAhead && base < r1) cur.load(a, t0, base, r1, q, sub);
+  if (kAhead && base < r1) cur.load(a, t0, base, r1, q, sub, ch);
   for (; base < r1; base += kStride) {
     BackRows<R, GATES> next;
     if constexpr (kAhead) {
-      if (base + kStride < r1) next.load(a, t0, base + kStride, r1, q, sub);
+      if (base + kStride < r1) next.load(a, t0, base + kStride, r1, q, sub, ch);
     } else {
-      cur.load(a, t0, base, r1, q, sub);
+      cur.load(a, t0, base, r1, q, sub, ch);
     }
-    cur.gather(a, t0, base, sub);
+    cur.gather(a, t0, base, ch);
     const Tops<R> tops(cur.x);
+    // the rows' sums and sums of w e
+    float sum[R::U], dot[R::U];
 #pragma unroll
     for (int u = 0; u < R::U; ++u) {
-      const long long t = t0 + base + u * R::ROWS + sub;
-      // the row's sum and sum of w e; with gates also the sums of the choices'
-      // e and of e dg
-      float v[GATES ? 4 : 2];
-      v[0] = tops.exp_row(u, cur.x[u]);
-      v[1] = 0.0f;
+      sum[u] = tops.exp_row(u, cur.x[u]);
+      dot[u] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) v[1] = fmaf(cur.x[u][i], wt[i], v[1]);
-      float g[R::J];
-      if constexpr (GATES) {
-        v[2] = v[3] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < R::J; ++j) {
-          g[j] = cur.id[u][j] >= 0 ? tops.exp(u, cur.xi[u][j]) : 0.0f;
-          v[2] += g[j];
-          v[3] = fmaf(g[j], cur.dg[u][j], v[3]);
-        }
-      }
+      for (int i = 0; i < R::N; ++i) dot[u] = fmaf(cur.x[u][i], wt[i], dot[u]);
+    }
+    if constexpr (R::U == 1) {
+      float v[2] = {sum[0], dot[0]};
       reduce_row<R::LANES>(v, Add());
-      const float sum = v[0];
-      const bool empty = sum == 0.0f;
-      const float inv = empty ? 0.0f : recip(sum);
-      // p_e (wt_e + shift)
-      const bool on = cur.in[u] && cur.valid[u] != 0 && !empty;
-      float shift = on ? fmaf(zq, tops.lse(u, sum), -v[1] * inv) : 0.0f;
-      float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
-      if constexpr (GATES) {
-        float gs = v[2], gd = v[3], ginv = inv;
+      sum[0] = v[0];
+      dot[0] = v[1];
+    } else {
+#pragma unroll
+      for (int u = 0; u < R::U; u += 2) {
+        float v[4] = {sum[u], dot[u], sum[u + 1], dot[u + 1]};
+        reduce_row<R::LANES>(v, Add());
+        sum[u] = v[0];
+        dot[u] = v[1];
+        sum[u + 1] = v[2];
+        dot[u + 1] = v[3];
+      }
+    }
+    float inv[R::U];
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      inv[u] = sum[u] == 0.0f ? 0.0f : recip(sum[u]);
+      if (GATES && !a.renorm && q == 0)
+        stat[u * R::ROWS + sub] = make_float2(tops.max[u], inv[u]);
+    }
+    if constexpr (GATES) {
+      if (!a.renorm) __syncwarp();
+#pragma unroll
+      for (int p = 0; p < BackRows<R, GATES>::ROUNDS; ++p) {
+        if (p >= ch.rounds) break;
+        const int row = ch.row(p);
+        const bool has = cur.id[p] >= 0;
+        float g = 0.0f, term;
         if (a.renorm) {
-          // choices so far below the row's maximum that they (nearly) underflow,
-          // as replayed ones may be: once more from their own maximum
-          if (__any_sync(0xffffffffu, cur.in[u] && gs < 1e-30f)) {
-            float m[1] = {cur.xi[u][0]};
-#pragma unroll
-            for (int j = 1; j < R::J; ++j) m[0] = fmaxf(m[0], cur.xi[u][j]);
-            reduce_row<R::LANES>(m, Max());
-            const float own = m[0] == -INFINITY ? 0.0f : m[0];
-            float w[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < R::J; ++j) {
-              g[j] = cur.id[u][j] >= 0 ? pow2((cur.xi[u][j] - own) * kLog2E) : 0.0f;
-              w[0] += g[j];
-              w[1] = fmaf(g[j], cur.dg[u][j], w[1]);
-            }
-            reduce_row<R::LANES>(w, Add());
-            gs = w[0];
-            gd = w[1];
-          }
-          ginv = gs == 0.0f ? 0.0f : recip(gs);
-        }
-        gd *= ginv;
-        if (!a.renorm) {
-          shift -= gd;
-          gd = 0.0f;
-        }
-        // whole warp: one choice a lane in each round
-#pragma unroll
-        for (int j = 0; j < R::J; ++j) {
-          if (R::LANES * j >= k) break;
-          const bool has = cur.id[u][j] >= 0;
-          const float v = g[j] * ginv * (cur.dg[u][j] - gd);
-          // a token's choices differ as a rule; given choices may repeat, and
-          // then their terms are added in the order of the choices
-          const unsigned same =
-              __match_any_sync(0xffffffffu, has ? sub * 1024 + cur.id[u][j] : -1 - lane);
-          if (__all_sync(0xffffffffu, __popc(same) == 1)) {
-            if (has) mine[cur.id[u][j]] += v;
-          } else {
-            for (int o = 0; o < R::LANES; ++o) {
-              if (has && q == o) mine[cur.id[u][j]] += v;
-              __syncwarp();
-            }
-          }
+          float own = ch.reduce(cur.xi[p], Max());
+          if (own == -INFINITY) own = 0.0f;
+          if (has) g = pow2((cur.xi[p] - own) * kLog2E);
+          const float gs = ch.reduce(g, Add());
+          const float gd = ch.reduce(g * cur.dg[p], Add());
+          const float ginv = gs == 0.0f ? 0.0f : recip(gs);
+          term = g * ginv * (cur.dg[p] - gd * ginv);
+        } else {
+          const float2 st = row < R::BATCH ? stat[row] : make_float2(0.0f, 0.0f);
+          if (has) g = tops.exp_of(st.x, cur.xi[p]) * st.y;
+          term = g * cur.dg[p];
+          const float gd = ch.reduce(term, Add());
           __syncwarp();
+          if (ch.c == 0 && row < R::BATCH) stat[row].x = gd;
+        }
+        // A token's choices differ as a rule, which every lane sees when it finds
+        // its own mark; given choices may repeat, and then their terms are added in
+        // the order of the choices.
+        float* at = sparse + (has ? row * R::WIDTH + cur.id[p] : 0);
+        if (has) *at = static_cast<float>(lane);
+        __syncwarp();
+        const bool own_mark = !has || *at == static_cast<float>(lane);
+        if (__all_sync(0xffffffffu, own_mark)) {
+          if (has) *at = term;
+        } else {
+          if (has) *at = 0.0f;
+          __syncwarp();
+          for (int o = 0; o < ch.span; ++o) {
+            if (has && ch.c == o) *at += term;
+            __syncwarp();
+          }
         }
       }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int r = base + u * R::ROWS + sub;
+      const bool in = r < r1;
+      // p_e (wt_e + shift)
+      const bool on = in && cur.valid[u] != 0 && sum[u] != 0.0f;
+      float shift = on ? fmaf(zq, tops.lse(u, sum[u]), -dot[u] * inv[u]) : 0.0f;
+      if (GATES && !a.renorm) shift -= stat[u * R::ROWS + sub].x;
       // a token that does not count gets zeros (whatever its logits hold) or
       // the gates' part alone
       float d[R::N];
 #pragma unroll
       for (int i = 0; i < R::N; ++i) {
-        const float v = (cur.x[u][i] * inv) * (on ? wt[i] + shift : shift);
+        const float v = (cur.x[u][i] * inv[u]) * (on ? wt[i] + shift : shift);
         d[i] = GATES || on ? v : 0.0f;
       }
       if constexpr (GATES) {
+        float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
         if constexpr (R::VEC) {
 #pragma unroll
           for (int v = 0; v < R::NV; ++v) {
@@ -686,10 +718,9 @@ __global__ void __launch_bounds__(kBackThreads)
             mine[c] = 0.0f;
           }
         }
-        __syncwarp();
       }
-      if (cur.in[u]) {
-        float* out = a.d_logits + t * a.ldd;
+      if (in) {
+        float* out = a.d_logits + (t0 + r) * a.ldd;
         if constexpr (R::VEC) {
 #pragma unroll
           for (int v = 0; v < R::NV; ++v) {
@@ -707,6 +738,7 @@ __global__ void __launch_bounds__(kBackThreads)
         }
       }
     }
+    if constexpr (GATES) __syncwarp();
     if constexpr (kAhead) cur = next;
   }
 }
@@ -745,7 +777,7 @@ cudaError_t loss_impl(const BalanceArgs& a, const BalanceScratch& w, cudaStream_
 template <class R, bool GATES>
 cudaError_t backward_impl(const RouterBackwardArgs& a, int sms, cudaStream_t s) {
   constexpr int warps = kBackThreads / 32;
-  const int smem = GATES ? warps * R::U * R::ROWS * R::WIDTH * 4 : 0;
+  const int smem = GATES ? warps * R::BATCH * (R::WIDTH + 2) * 4 : 0;
   static int resident_of[kMaxDevices] = {};
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
