@@ -47,7 +47,7 @@ struct Row {
   static constexpr int U = NV >= 3 ? 1 : 4 / NV;  // of those in flight
   static constexpr int BATCH = ROWS * U;
   static constexpr int WIDTH = LANES * N;       // columns covered, >= E
-  static constexpr int J = (16 + LANES - 1) / LANES;  // choices a lane (k <= 16)
+  static constexpr int J = (16 + LANES - 1) / LANES;  // choices a lane (loss; k <= 16)
   // column of element i of lane q
   __device__ static __forceinline__ int col(int q, int i) {
     return VEC ? 4 * (q + LANES * (i >> 2)) + (i & 3) : q + LANES * i;

@@ -113,6 +113,17 @@ long long tiles(long long M, long long N, int shape) {
   return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
 }
 
+// Into how many parts gram's k-blocks are split: a few tiles with a long K (the
+// gradient of a router or a projection to a small latent) would leave most SMs
+// idle. A part has 8 k-blocks or more, because joining the parts (through L2)
+// costs about as much as 12.
+int gram_split(long long batch, long long side, int k_gram, int sms, int shape) {
+  if (shape == lmoe::kNsPair) return 1;
+  const long long free_sms = sms / (batch * sym_tiles(side, shape));
+  const long long most = free_sms < k_gram / 8 ? free_sms : k_gram / 8;
+  return static_cast<int>(most < 1 ? 1 : most > 8 ? 8 : most);
+}
+
 // Rounds of tiles decide the shape: a round takes its k-blocks and, once a phase,
 // the hand-over of the results to the next phase. In ns, measured: a k-block 270
 // (narrow), 320 (single), 310 (pair): an SM takes in about 64 bytes a clock, which
@@ -125,8 +136,10 @@ int pick_shape(const latentmoe_muon* h) {
   const NsArgs& a = h->args;
   const auto cost = [&](int shape, long long units, long long block, long long hand_over) {
     const long long sym = (sym_tiles(h->side, shape) * h->batch + units - 1) / units;
+    const int split = gram_split(h->batch, h->side, a.k_gram, h->sms, shape);
+    const long long gram = (a.k_gram + split - 1) / split + (split > 1 ? 12 : 0);
     const long long app = (tiles(h->rows, h->cols, shape) * h->batch + units - 1) / units;
-    return (sym * (a.k_gram + a.k_side) + app * a.k_side) * block + 3 * hand_over;
+    return (sym * (gram + a.k_side) + app * a.k_side) * block + 3 * hand_over;
   };
   const long long narrow = cost(lmoe::kNsNarrow, h->sms, 270, 4200);
   const long long single = cost(lmoe::kNsSingle, h->sms, 320, 5400);
@@ -172,13 +185,14 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
   }
   NS_CK(h, lmoe::launch_ns_norm(u, h->batch, n, h->chunks, h->chunk, h->partial, s));
   NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, a.ld_x, h->chunks, h->partial,
-                                h->eps, h->scale0, h->x32, h->x16, a.done, 3 * a.steps, a.counter, s));
+                                h->eps, h->scale0, h->x32, h->x16, a.done, a.done_ld, a.counter, s));
   h->launches += 2;
   const int shape = pick_shape(h);
   const long long bm = lmoe::ns_bm(shape);
   a.sym_tiles = static_cast<int>(sym_tiles(h->side, shape));
   a.m_tiles = static_cast<int>((h->rows + bm - 1) / bm);
   a.apply_tiles = static_cast<int>(tiles(h->rows, h->cols, shape));
+  a.split = gram_split(h->batch, h->side, a.k_gram, h->sms, shape);
   a.group = h->group;
   a.out_mode = out_mode;
   a.out = out;
@@ -312,7 +326,21 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   const size_t o_gram = take(an * 2), o_poly = take(an * 2);
   const size_t o_da = take(static_cast<size_t>(B) * lda * 4);
   const size_t o_dp = take(static_cast<size_t>(B) * lda * 4);
-  const size_t o_done = take(static_cast<size_t>(B) * 3 * h->steps * 4), o_counter = take(16);
+  // the parts of a split gram product, in either shape that may be asked for
+  size_t parts = 0;
+  a.done_ld = 3 * h->steps;
+  for (int shape : {lmoe::kNsSingle, lmoe::kNsNarrow}) {
+    const long long split = gram_split(B, side, a.k_gram, h->sms, shape);
+    if (split == 1) continue;
+    const long long n_tiles = sym_tiles(side, shape);
+    const size_t need = static_cast<size_t>(B * n_tiles * split) * lmoe::ns_bm(shape) *
+                        lmoe::ns_bn(shape) * 4;
+    if (need > parts) parts = need;
+    const long long ld = 3 * h->steps + n_tiles * lmoe::kNsEpiWarps;
+    if (ld > a.done_ld) a.done_ld = static_cast<int>(ld);
+  }
+  const size_t o_parts = take(parts);
+  const size_t o_done = take(static_cast<size_t>(B) * a.done_ld * 4), o_counter = take(16);
   const size_t o_partial = take(static_cast<size_t>(B) * h->chunks * 4), o_status = take(16);
   e = cudaMalloc(&h->ws, off);
   if (e != cudaSuccess) {
@@ -328,6 +356,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   void* poly = base + o_poly;
   a.diag_a = reinterpret_cast<float*>(base + o_da);
   a.diag_p = reinterpret_cast<float*>(base + o_dp);
+  a.parts = reinterpret_cast<float*>(base + o_parts);
   a.done = reinterpret_cast<int*>(base + o_done);
   a.counter = reinterpret_cast<int*>(base + o_counter);
   a.status = reinterpret_cast<unsigned*>(base + o_status);

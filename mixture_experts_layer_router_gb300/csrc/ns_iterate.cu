@@ -4,7 +4,7 @@
 
 namespace lmoe {
 
-template <int SHAPE>
+template <int SHAPE, bool SPLIT>
 static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cudaStream_t s) {
   constexpr bool PAIR = SHAPE == kNsPair;
   static int units_of[kMaxDevices] = {};
@@ -13,7 +13,8 @@ static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cud
   int& most = units_of[dev];
   if (most == 0) {
     cudaError_t e = cudaFuncSetAttribute(
-        ns_iterate_kernel<SHAPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, ns_smem_bytes(SHAPE));
+        ns_iterate_kernel<SHAPE, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        ns_smem_bytes(SHAPE));
     if (e != cudaSuccess) return e;
     int n = sms;
     if (PAIR) {
@@ -30,7 +31,7 @@ static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cud
       cfg.dynamicSmemBytes = ns_smem_bytes(SHAPE);
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n, ns_iterate_kernel<SHAPE>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, ns_iterate_kernel<SHAPE, SPLIT>, &cfg);
       if (e != cudaSuccess) return e;
       if (n > sms / 2) n = sms / 2;
     }
@@ -38,21 +39,22 @@ static cudaError_t launch_ns_impl(const NsMaps& m, const NsArgs& a, int sms, cud
     most = n;
   }
   // no more units than the widest phase of all matrices in flight has tiles
-  const long long wide = static_cast<long long>(a.sym_tiles > a.apply_tiles ? a.sym_tiles
-                                                                            : a.apply_tiles) *
-                         a.batch;
+  const long long sym = static_cast<long long>(a.sym_tiles) * a.split;
+  const long long wide = (sym > a.apply_tiles ? sym : a.apply_tiles) * a.batch;
   const int units = static_cast<int>(wide < most ? wide : most);
-  return launch_kernel(ns_iterate_kernel<SHAPE>, dim3(static_cast<unsigned>(PAIR ? 2 * units : units)),
-                       dim3(kNsThreads), ns_smem_bytes(SHAPE), s, PAIR ? 2 : 1, false, m, a);
+  return launch_kernel(ns_iterate_kernel<SHAPE, SPLIT>,
+                       dim3(static_cast<unsigned>(PAIR ? 2 * units : units)), dim3(kNsThreads),
+                       ns_smem_bytes(SHAPE), s, PAIR ? 2 : 1, false, m, a);
 }
 
 cudaError_t launch_ns_iterate(int shape, const NsMaps& m, const NsArgs& a, int sms,
                               cudaStream_t s) {
-  switch (shape) {
-    case kNsPair: return launch_ns_impl<kNsPair>(m, a, sms, s);
-    case kNsSingle: return launch_ns_impl<kNsSingle>(m, a, sms, s);
-    default: return launch_ns_impl<kNsNarrow>(m, a, sms, s);
-  }
+  if (shape == kNsPair) return launch_ns_impl<kNsPair, false>(m, a, sms, s);
+  if (shape == kNsSingle)
+    return a.split > 1 ? launch_ns_impl<kNsSingle, true>(m, a, sms, s)
+                       : launch_ns_impl<kNsSingle, false>(m, a, sms, s);
+  return a.split > 1 ? launch_ns_impl<kNsNarrow, true>(m, a, sms, s)
+                     : launch_ns_impl<kNsNarrow, false>(m, a, sms, s);
 }
 
 }  // namespace lmoe

@@ -138,10 +138,14 @@ struct NsArgs {
   int sym_tiles;       // of gram and poly
   int m_tiles, apply_tiles;
   int k_gram, k_side;  // k-blocks of gram, of poly and apply
+  int split;           // parts of gram's k-blocks, each a tile of its own
   long long ld_x, ld_a;
   float* diag_a;       // [batch, ld_a]
   float* diag_p;
-  int* done;           // [batch, 3 steps] epilogue warps that have stored
+  float* parts;        // [batch, sym_tiles, split, tile] gram's partial sums (split > 1)
+  int* done;           // a matrix: [3 steps] epilogue warps that have stored, then
+                       // [sym_tiles, kNsEpiWarps] warps that have left partial sums
+  int done_ld;
   int* counter;        // next tile of the sequence
   int out_mode;
   void* out;           // [batch, rows, cols] contiguous
@@ -205,12 +209,15 @@ struct NsTile {
   int step, phase;
   int row0, col0;  // of the result
   bool mirror;     // symmetric result, tile below the diagonal
+  int tile, part;  // gram: of the matrix, of its k-blocks
+  int kb0, kbs;    // first k-block and how many
 };
 
-template <int SHAPE>
+template <int SHAPE, bool SPLIT>
 __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
   NsTile c;
-  const int per_step = 2 * a.sym_tiles + a.apply_tiles;  // of one matrix
+  const int split = SPLIT ? a.split : 1;
+  const int per_step = (split + 1) * a.sym_tiles + a.apply_tiles;  // of one matrix
   const int per_group = a.group * a.steps * per_step;
   const int g = t / per_group;
   const int first = g * a.group;
@@ -218,11 +225,12 @@ __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
   int r = t - g * per_group;
   c.step = r / (n * per_step);
   r -= c.step * n * per_step;
-  int tiles = a.sym_tiles;
+  int tiles = split * a.sym_tiles;
   c.phase = kNsGram;
   if (r >= n * tiles) {
     r -= n * tiles;
     c.phase = kNsPoly;
+    tiles = a.sym_tiles;
     if (r >= n * tiles) {
       r -= n * tiles;
       c.phase = kNsApply;
@@ -231,7 +239,17 @@ __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
   }
   const int mi = r / tiles;
   c.b = first + mi;
-  const int local = r - mi * tiles;
+  int local = r - mi * tiles;
+  c.part = 0;
+  c.kb0 = 0;
+  c.kbs = c.phase == kNsGram ? a.k_gram : a.k_side;
+  if (SPLIT && c.phase == kNsGram) {
+    c.part = local % split;
+    local /= split;
+    c.kb0 = c.part * a.k_gram / split;
+    c.kbs = (c.part + 1) * a.k_gram / split - c.kb0;
+  }
+  c.tile = local;
   constexpr int BM = ns_bm(SHAPE), BN = ns_bn(SHAPE);
   constexpr int R = BM / BN;  // tiles across a square of the diagonal
   int i, j;
@@ -501,7 +519,7 @@ __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-template <int SHAPE>
+template <int SHAPE, bool SPLIT>
 __global__ void __launch_bounds__(kNsThreads, 1)
     ns_iterate_kernel(const __grid_constant__ NsMaps tm, const __grid_constant__ NsArgs a) {
   constexpr bool PAIR = SHAPE == kNsPair;
@@ -570,7 +588,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   auto wait_phase = [&](const NsTile& c) {
     if (c.step == 0 && c.phase == kNsGram) return true;
     const int before = 3 * c.step + c.phase - 1;
-    const int* p = a.done + static_cast<long long>(c.b) * (3 * a.steps) + before;
+    const int* p = a.done + static_cast<long long>(c.b) * a.done_ld + before;
     const int want = kStores * (c.phase == kNsGram ? a.apply_tiles : a.sym_tiles);
     if (ld_acquire_gpu(p) >= want) return true;
     const uint64_t t0 = global_timer_ns();
@@ -630,7 +648,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   tc_fence_after_sync();
 
   const uint32_t tmem_base = *tmem_slot;
-  const int total = a.batch * a.steps * (2 * a.sym_tiles + a.apply_tiles);
+  const int total =
+      a.batch * a.steps * (((SPLIT ? a.split : 1) + 1) * a.sym_tiles + a.apply_tiles);
   const uint32_t tr_empty_leader = PAIR ? mapa_shared(smem_addr(&tr_empty[0]), 0) : 0u;
 
   auto read_tile = [&](int& slot, uint32_t& ph) -> int {
@@ -675,7 +694,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           t = read_tile(slot, slot_ph);
         }
         if (t < 0) break;
-        const NsTile c = ns_decode<SHAPE>(t, a);
+        const NsTile c = ns_decode<SHAPE, SPLIT>(t, a);
         const CUtensorMap* mx = &tm.x[c.step & 1];
         const CUtensorMap* ma = c.phase == kNsPoly ? &tm.gram : mx;
         const CUtensorMap* mb = ma;
@@ -689,7 +708,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         const int arow = c.row0 + rank * 128;
         const int brow = c.col0 + rank * 128;
-        const int kbs = c.phase == kNsGram ? a.k_gram : a.k_side;
+        const int kbs = c.kbs;
         const int ahead = kbs > kNsStages ? kbs - kNsStages : 0;
         if (!wait_phase(c)) break;
         fence_proxy_async_global();
@@ -705,9 +724,10 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           const uint32_t fb = PAIR ? mapa_shared(smem_addr(&full_bar[stage]), 0) : 0u;
           if (leader)
             mbar_arrive_expect_tx(&full_bar[stage], (PAIR ? 2u : 1u) * kNsStageBytes);
-          ns_load<PAIR, 128>(ma, amn, &full_bar[stage], fb, sa, arow, kb * kNsBK, c.b, pol);
-          ns_load<PAIR, kBRows>(mb, bmn, &full_bar[stage], fb, sa + kNsTileBytes, brow, kb * kNsBK, c.b,
-                        pol);
+          ns_load<PAIR, 128>(ma, amn, &full_bar[stage], fb, sa, arow, (c.kb0 + kb) * kNsBK, c.b,
+                             pol);
+          ns_load<PAIR, kBRows>(mb, bmn, &full_bar[stage], fb, sa + kNsTileBytes, brow,
+                                (c.kb0 + kb) * kNsBK, c.b, pol);
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == kNsStages) {
@@ -733,14 +753,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       while (ok) {
         const int t = read_tile(slot, slot_ph);
         if (t < 0) break;
-        const NsTile c = ns_decode<SHAPE>(t, a);
+        const NsTile c = ns_decode<SHAPE, SPLIT>(t, a);
         const bool amn = c.phase == kNsGram && a.tall != 0;
         const bool bmn = c.phase == kNsGram ? amn : c.phase == kNsApply && a.tall == 0;
         const uint32_t idesc = instr_desc_f16(kBM, kBN, amn, bmn);
         // 16 elements of K: 32 bytes along a K-major row, 16 rows of 128 bytes otherwise
         const uint64_t step_a = amn ? 128ull : 2ull;
         const uint64_t step_b = bmn ? 128ull : 2ull;
-        const int kbs = c.phase == kNsGram ? a.k_gram : a.k_side;
+        const int kbs = c.kbs;
         if (!wait1(&tempty_bar[acc], acc_phase ^ 1u)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
@@ -797,7 +817,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       if (lane == 0) t = read_tile(slot, slot_ph);
       t = __shfl_sync(0xffffffffu, t, 0);
       if (t < 0) break;
-      const NsTile c = ns_decode<SHAPE>(t, a);
+      const NsTile c = ns_decode<SHAPE, SPLIT>(t, a);
       const NsStep& f = a.step[c.step];
       const bool sym = c.phase != kNsApply;
       const bool poly = c.phase == kNsPoly;
@@ -848,72 +868,140 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc * kBN + half * 32);
       bool ok = true;
-      for (int i = 0; i < chunks; ++i) {
-        const int col = col0 + 64 * i;
-        const int sl = i % kSlots;
-        uint8_t* sx = my_slots + sl * kNsX;
-        uint8_t* sh = my_slots + kSlots * kNsX + sl * kNsH;
-        uint32_t v[32];
-        tmem_ld_32cols(tbase + static_cast<uint32_t>(64 * i), v);
-        if (cols_differ) {
-          coef[lane] = poly ? f.poly_c * by_col : fmaf(f.d_x, by_col, f.a_x);
-          load_col(i + 1);
-        }
-        if (lane == 0) {
-          if (c.phase == kNsGram) {
-            bulk_wait_read<1>();  // the chunk before last has left this slot
-          } else if (i > 0 && i + 1 < chunks) {
-            // the last chunk has left its slot: bring in the next one
-            if (!last) bulk_wait_read<0>();
-            load_chunk(i + 1);
-          }
-        }
-        if (c.phase != kNsGram) {
-          if (!wait32(&my_bars[sl], (bar_ph >> sl) & 1u)) {
-            ok = false;
-            break;
-          }
-          bar_ph ^= 1u << sl;
-          if (lane == 0) in_flight &= ~(1u << sl);
-        }
-        __syncwarp();
-        tmem_ld_wait();
-        if (i + 1 == chunks) {
-          // the accumulators are free
-          tc_fence_before_sync();
+      // a part of gram's k-blocks: every chunk's sums to memory (turn 0); the warp
+      // that comes last for its rows adds the parts and goes on with them (turn 1)
+      const bool joined = SPLIT && c.phase == kNsGram;
+      bool mine = true;  // this warp's results are the tile's
+      float4* parts = nullptr;
+      if constexpr (SPLIT) {
+        if (joined)
+          parts = reinterpret_cast<float4*>(a.parts) +
+                  (static_cast<long long>(c.b * a.sym_tiles + c.tile) * a.split) *
+                      (kBM * kBN / 4) +
+                  (warp - 2) * (kBN / 64) * 256 + lane;
+      }
+      for (int turn = joined ? 0 : 1; turn < 2 && mine && ok; ++turn) {
+        if (joined && turn == 1) {
+          // in the order of the parts, so the sum does not depend on who adds it
+          int last_in = 0;
           __syncwarp();
           if (lane == 0) {
-            if constexpr (PAIR) mbar_arrive_relaxed_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
-            else mbar_arrive(&tempty_bar[acc]);
+            __threadfence();
+            const int n = atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 3 * a.steps +
+                                        c.tile * kNsEpiWarps + (warp - 2),
+                                    1);
+            __threadfence();
+            last_in = (n + 1) % a.split == 0 ? 1 : 0;
           }
+          mine = __shfl_sync(0xffffffffu, last_in, 0) != 0;
+          if (!mine) break;
         }
-        if (sym) {
-          ns_sym_chunk(a, f, c, sx, coef, v, row, col, by_row);
-        } else if (last) {
-          if (a.tall) ns_apply_chunk<true, true>(f.apply_acc, by_row, coef, sx, sh, v);
-          else ns_apply_chunk<false, true>(f.apply_acc, by_row, coef, sx, sh, v);
+        for (int i = 0; i < chunks; ++i) {
+          const int col = col0 + 64 * i;
+          const int sl = i % kSlots;
+          uint8_t* sx = my_slots + sl * kNsX;
+          uint8_t* sh = my_slots + kSlots * kNsX + sl * kNsH;
+          uint32_t v[32];
+          if (joined && turn == 1) {
+            float sum[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sum[k] = 0.0f;
+            // two parts at a time on their way
+            for (int p = 0; p < a.split; p += 2) {
+              float4 w[2][8];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float4* from =
+                    parts + static_cast<long long>(p + h) * (kBM * kBN / 4) + i * 256;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  w[h][k] = p + h < a.split ? __ldcg(from + 32 * k)
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  sum[4 * k] += w[h][k].x;
+                  sum[4 * k + 1] += w[h][k].y;
+                  sum[4 * k + 2] += w[h][k].z;
+                  sum[4 * k + 3] += w[h][k].w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(sum[k]);
+          } else {
+            tmem_ld_32cols(tbase + static_cast<uint32_t>(64 * i), v);
+          }
+          if (cols_differ) {
+            coef[lane] = poly ? f.poly_c * by_col : fmaf(f.d_x, by_col, f.a_x);
+            load_col(i + 1);
+          }
+          if (lane == 0) {
+            if (c.phase == kNsGram) {
+              bulk_wait_read<1>();  // the chunk before last has left this slot
+            } else if (i > 0 && i + 1 < chunks) {
+              // the last chunk has left its slot: bring in the next one
+              if (!last) bulk_wait_read<0>();
+              load_chunk(i + 1);
+            }
+          }
+          if (c.phase != kNsGram) {
+            if (!wait32(&my_bars[sl], (bar_ph >> sl) & 1u)) {
+              ok = false;
+              break;
+            }
+            bar_ph ^= 1u << sl;
+            if (lane == 0) in_flight &= ~(1u << sl);
+          }
           __syncwarp();
-          ns_put_out(a, c.b, sx, row, col);
-          // the slot's next contents come by TMA
+          tmem_ld_wait();
+          if (i + 1 == chunks && !(joined && turn == 1)) {
+            // the accumulators are free
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR)
+                mbar_arrive_relaxed_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
+              else mbar_arrive(&tempty_bar[acc]);
+            }
+          }
+          if (joined && turn == 0) {
+            float4* to = parts + static_cast<long long>(c.part) * (kBM * kBN / 4) + i * 256;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              to[32 * k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                       __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+            continue;
+          }
+          if (sym) {
+            ns_sym_chunk(a, f, c, sx, coef, v, row, col, by_row);
+          } else if (last) {
+            if (a.tall) ns_apply_chunk<true, true>(f.apply_acc, by_row, coef, sx, sh, v);
+            else ns_apply_chunk<false, true>(f.apply_acc, by_row, coef, sx, sh, v);
+            __syncwarp();
+            ns_put_out(a, c.b, sx, row, col);
+            // the slot's next contents come by TMA
+            fence_async_smem();
+            __syncwarp();
+            continue;
+          } else {
+            if (a.tall) ns_apply_chunk<true, false>(f.apply_acc, by_row, coef, sx, sh, v);
+            else ns_apply_chunk<false, false>(f.apply_acc, by_row, coef, sx, sh, v);
+          }
           fence_async_smem();
           __syncwarp();
-          continue;
-        } else {
-          if (a.tall) ns_apply_chunk<true, false>(f.apply_acc, by_row, coef, sx, sh, v);
-          else ns_apply_chunk<false, false>(f.apply_acc, by_row, coef, sx, sh, v);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (sym) {
-            const CUtensorMap* to = poly ? &tm.chunk_poly : &tm.chunk_gram;
-            tma_store_3d(to, sx, col, row, c.b);
-            if (c.mirror) tma_store_3d(to, sx + kNsH, row, col, c.b);
-          } else {
-            tma_store_3d(&tm.chunk_x, sx, col, row, c.b);
-            tma_store_3d(&tm.chunk_h[(c.step + 1) & 1], sh, col, row, c.b);
+          if (lane == 0) {
+            if (sym) {
+              const CUtensorMap* to = poly ? &tm.chunk_poly : &tm.chunk_gram;
+              tma_store_3d(to, sx, col, row, c.b);
+              if (c.mirror) tma_store_3d(to, sx + kNsH, row, col, c.b);
+            } else {
+              tma_store_3d(&tm.chunk_x, sx, col, row, c.b);
+              tma_store_3d(&tm.chunk_h[(c.step + 1) & 1], sh, col, row, c.b);
+            }
+            bulk_commit();
           }
-          bulk_commit();
         }
       }
       if (!ok) break;
@@ -921,17 +1009,18 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (PAIR) mbar_arrive_relaxed_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
+          if constexpr (PAIR)
+            mbar_arrive_relaxed_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
           else mbar_arrive(&tempty_bar[acc]);
         }
       }
-      if (!last) {
+      if (!last && mine) {
         // this warp's part is in memory: count it for the next phase's tiles
         __syncwarp();
         if (lane == 0) {
           bulk_wait_all();
           __threadfence();
-          atomicAdd(a.done + static_cast<long long>(c.b) * (3 * a.steps) + 3 * c.step + c.phase, 1);
+          atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 3 * c.step + c.phase, 1);
         }
       }
       if (++acc == 2) {

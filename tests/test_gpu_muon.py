@@ -113,6 +113,27 @@ def test_zeros_nan_and_infinity_stay_in_their_matrix(rows, cols):
     assert m.status() == 0
 
 
+# few tiles and a long side: the first product of a step is split over its k
+@pytest.mark.parametrize("pairs", [0, 2, 3])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 256, 7168), (1, 7168, 256), (2, 33, 4200),
+                                             (1, 200, 2000), (3, 150, 1025), (1, 8704, 64),
+                                             (1, 1, 20000), (7, 260, 1600)])
+def test_long_sides(batch, rows, cols, pairs):
+    gh.lib()
+    m = capi.Muon(rows, cols, batch=batch)
+    m.set_sm_pairs(pairs)
+    g = rand((batch, rows, cols), rows + cols).to(torch.bfloat16)
+    o = m.orthogonalize(g)
+    assert m.status() == 0
+    assert rel(o, newton_schulz(g)) <= TOL
+    for _ in range(3):  # the sum does not depend on which part comes last
+        assert torch.equal(o, m.orthogonalize(g))
+    bad = g.clone()
+    bad[batch - 1, rows - 1, cols - 1] = float("nan")
+    x = m.orthogonalize(bad)
+    assert torch.equal(x[:-1], o[:-1]) and torch.isnan(x[-1]).all()
+
+
 @pytest.mark.parametrize("rows,cols", [(100, 300), (300, 200)])
 @pytest.mark.parametrize("scale", [1e-15, 1e-6, 1.0, 1e12])
 def test_scale_of_the_update(rows, cols, scale):
