@@ -40,8 +40,7 @@
 // that running CTAs take from a counter (groups of matrices; in a group: steps,
 // phases, matrices, tiles), and a tile waits until every tile of its matrix's
 // preceding phase has been stored (a count per matrix and phase). While one
-// matrix waits, tiles of the others run; a group is as many matrices as stay in
-// L2 from phase to phase. Progress: tiles are taken in sequence order by running
+// matrix waits, tiles of the others run. Progress: tiles are taken in sequence order by running
 // CTAs alone and wait only for earlier ones, so the earliest unfinished tile can
 // always proceed. No buffer is overwritten early: a phase's inputs were read by
 // phases that its own predecessor has waited for.
@@ -55,6 +54,21 @@
 //           decides: 24 KB a k-block (an SM takes in about 64 bytes a clock,
 //           which is what the mainloops of single tiles are bound by) and half
 //           as many results to store
+// SPLIT (single and narrow): gram's k-blocks in `split` parts, each a tile of its
+// own, for few tiles with a long K (a router's gradient). The parts' fp32 sums go
+// to memory, and the warp that comes last for its 32 rows adds them in the order
+// of the parts. 64 x 8704 253 -> 110 us, 200 x 2000 118 -> 104 us. An
+// instantiation of its own: as a branch it cost the others 4 %.
+//
+// What bounds it. Pairs: the MMA rate at the clock the power cap leaves (about
+// 1.46 GHz under this load) and, in apply, the operands and the fp32 X that come
+// through L2 at 13 TB/s in all; 8 x 1024 x 2048: 392 us, 575 MB read
+// and 578 MB written in DRAM, tensor pipe busy 36 % of the time; 64 x 2048 x 1024:
+// 2.82 ms, 0.85 PFLOP/s of the 2.41 TFLOP that the symmetric form needs;
+// 4096 x 8704 with the step around it: 2.17 ms, 1.17 PFLOP/s. Single
+// and narrow: the hand-over between phases (4 to 5 us: last store, count, first
+// load, ring, epilogue) and the 64 bytes a clock that an SM takes in:
+// 3 x 777 x 1333 213 us, 1024 x 1024 147 us, 512 x 512 103 us.
 //
 //   warp 0      TMA producer (one lane), takes and publishes the tiles
 //   warp 1      TMEM allocator, MMA issuer (one lane; pair: the leader's)
