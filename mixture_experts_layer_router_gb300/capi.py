@@ -189,6 +189,16 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _on_stream(stream, call, *args, **kw):
+    """call(..., stream=None) with ``stream`` as the current one, so that the outputs
+    it allocates are that stream's: memory whose last use on the caller's current
+    stream has not ended yet is not handed out to them. Inputs made on another
+    stream are the caller's to wait for and to record, as everywhere in torch."""
+    import torch
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
 _raw_stream = None  # () -> handle of the current stream
 
 
@@ -368,6 +378,9 @@ class LatentMoE:
         "prob_sum" [S, E], "z_sum" [S], "tokens" [S] int32} over S = T /
         seq_len sequences (0: one)."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.balance_loss, logits, idx, valid, seq_len,
+                              balance_coef, z_coef)
         T, E = logits.shape[0], self.dims.num_experts
         ld = self._rows(logits, "logits", T)
         self._per_slot(idx, "idx", T, torch.int32)
@@ -379,7 +392,7 @@ class LatentMoE:
                                      tokens.data_ptr())
         check(load().latentmoe_balance_loss(
             self.handle, logits.data_ptr(), ld, idx.data_ptr(), self._valid(valid, T), T, seq_len,
-            balance_coef, z_coef, ctypes.byref(st), loss.data_ptr(), _stream(stream)),
+            balance_coef, z_coef, ctypes.byref(st), loss.data_ptr(), _stream(None)),
             "latentmoe_balance_loss", self.handle)
         return {"loss": loss, "counts": counts, "prob_sum": prob, "z_sum": z, "tokens": tokens}
 
@@ -387,6 +400,8 @@ class LatentMoE:
                                 stream=None):
         """loss [3] from (summed) stats as returned by balance_loss."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.balance_loss_from_stats, stats, balance_coef, z_coef)
         c = stats["counts"]
         S, E = c.shape[0], self.dims.num_experts
         for name, shape, dt in (("counts", (S, E), torch.int32), ("prob_sum", (S, E), torch.float32),
@@ -399,7 +414,7 @@ class LatentMoE:
                                        ("counts", "prob_sum", "z_sum", "tokens")))
         check(load().latentmoe_balance_loss_from_stats(self.handle, ctypes.byref(st), S,
                                                        balance_coef, z_coef, loss.data_ptr(),
-                                                       _stream(stream)),
+                                                       _stream(None)),
               "latentmoe_balance_loss_from_stats", self.handle)
         return loss
 
@@ -408,6 +423,9 @@ class LatentMoE:
                         d_loss=None, out=None, stream=None):
         """d logits [T, E] fp32 of d_loss * loss[0] + sum d_gates * gates."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.router_backward, logits, idx, counts, tokens, d_gates,
+                              valid, seq_len, balance_coef, z_coef, d_loss, out)
         T, E = logits.shape[0], self.dims.num_experts
         ld = self._rows(logits, "logits", T)
         S = self._sequences(T, seq_len)
@@ -427,7 +445,7 @@ class LatentMoE:
         check(load().latentmoe_router_backward(
             self.handle, logits.data_ptr(), ld, _ptr(idx), _ptr(d_gates), self._valid(valid, T),
             counts.data_ptr(), tokens.data_ptr(), T, seq_len, balance_coef, z_coef, _ptr(d_loss),
-            out.data_ptr(), self._rows(out, "out", T), _stream(stream)),
+            out.data_ptr(), self._rows(out, "out", T), _stream(None)),
             "latentmoe_router_backward", self.handle)
         return out
 
@@ -593,6 +611,8 @@ class Muon:
     def orthogonalize(self, g, out=None, stream=None):
         """The orthogonalised g (bf16 or fp32), in bf16."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.orthogonalize, g, out)
         self._matrices(g, "g")
         if out is None:
             out = torch.empty_like(g, dtype=torch.bfloat16)
@@ -600,7 +620,7 @@ class Muon:
             self._matrices(out, "out")
             _need(out.dtype == torch.bfloat16, "out must be bfloat16")
         self._check(load().latentmoe_muon_orthogonalize(
-            self.handle, g.data_ptr(), _dtype_code(g, "g"), out.data_ptr(), _stream(stream)),
+            self.handle, g.data_ptr(), _dtype_code(g, "g"), out.data_ptr(), _stream(None)),
             "latentmoe_muon_orthogonalize")
         return out
 

@@ -445,3 +445,27 @@ def test_offsets_beyond_32_bits():
     ref = p * (w - dot + q * lse)
     size = p * (w + dot + q * lse.abs())
     assert bool(((d[-3:].double() - ref).abs() <= G_TOL * size + 1e-30).all())
+
+
+def test_outputs_of_another_stream_do_not_take_memory_in_use():
+    """Memory freed on the current stream, where a kernel has still to write it, is
+    not handed to the outputs of a call on another stream."""
+    T, E, k = 512, 64, 4
+    L = layer(E, k, T)
+    logits, idx, _, dg = inputs(T, E, k, 5)
+    want = L.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC)
+    grad = L.router_backward(logits, idx, want["counts"], want["tokens"], d_gates=dg)
+    torch.empty(3, device="cuda").fill_(7.0)  # loads the fill kernel
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # 10 ms at 2 GHz
+    for shape in ((T, E), (1, E), (3,), (1,)):
+        late = [torch.empty(shape, device="cuda").fill_(7.0) for _ in range(4)]
+        del late
+    got = L.balance_loss(logits, idx, balance_coef=BC, z_coef=ZC, stream=side)
+    loss = L.balance_loss_from_stats(got, balance_coef=BC, z_coef=ZC, stream=side)
+    d = L.router_backward(logits, idx, got["counts"], got["tokens"], d_gates=dg, stream=side)
+    torch.cuda.synchronize()
+    for key in want:
+        assert torch.equal(got[key], want[key]), key
+    assert torch.equal(d, grad) and rel(loss, want["loss"].double()) <= L_TOL

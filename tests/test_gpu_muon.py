@@ -311,3 +311,18 @@ def test_offsets_beyond_32_bits():
     for b in (0, batch - 1):
         assert rel(o[b], newton_schulz(g[b])) <= TOL
     assert not bool(o[1:batch - 1].any())
+
+
+def test_output_of_another_stream_does_not_take_memory_in_use():
+    m = capi.Muon(300, 200)
+    g = rand((300, 200), 3)
+    want = m.orthogonalize(g)
+    torch.empty_like(want).fill_(7.0)  # loads the fill kernel
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # 10 ms at 2 GHz
+    late = [torch.empty_like(want).fill_(7.0) for _ in range(4)]
+    del late
+    o = m.orthogonalize(g, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
