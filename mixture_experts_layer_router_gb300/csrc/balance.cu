@@ -277,6 +277,18 @@ __global__ void __launch_bounds__(kBalThreads, 1)
   const int q = lane % R::LANES, sub = lane / R::LANES;
   const int E = a.E, k = a.k;
   const int units = a.seqs * parts;
+  // the loss from the sequences', by the CTA that arrives last of n
+  auto last_sequence = [&](unsigned n) {
+    if (!arrive_last(w.ticket + 2 * w.units, n, &flag)) return;
+    float bs = 0.0f, zs = 0.0f;
+    for (int i = threadIdx.x; i < a.seqs; i += kBalThreads) {
+      bs += __ldcg(w.seq + 2ll * i);
+      zs += __ldcg(w.seq + 2ll * i + 1);
+    }
+    bs = block_sum(bs, buf) / static_cast<float>(a.seqs);
+    zs = block_sum(zs, buf) / static_cast<float>(a.seqs);
+    if (threadIdx.x == 0) store_loss(a.loss, bs, zs, a.balance_coef, a.z_coef);
+  };
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int s = unit / parts, part = unit - s * parts;
     for (int e = threadIdx.x; e < E; e += kBalThreads) hist[e] = 0;
@@ -451,20 +463,13 @@ __global__ void __launch_bounds__(kBalThreads, 1)
           w.seq[2ll * s] = balance;
           w.seq[2ll * s + 1] = zmean;
         }
-        if (arrive_last(w.ticket + 2 * w.units, static_cast<unsigned>(a.seqs), &flag)) {
-          float bs = 0.0f, zs = 0.0f;
-          for (int i = threadIdx.x; i < a.seqs; i += kBalThreads) {
-            bs += __ldcg(w.seq + 2ll * i);
-            zs += __ldcg(w.seq + 2ll * i + 1);
-          }
-          bs = block_sum(bs, buf) / static_cast<float>(a.seqs);
-          zs = block_sum(zs, buf) / static_cast<float>(a.seqs);
-          if (e == 0) store_loss(a.loss, bs, zs, a.balance_coef, a.z_coef);
-        }
+        if (parts > 1) last_sequence(static_cast<unsigned>(a.seqs));
       }
     }
     __syncthreads();
   }
+  // a CTA with whole sequences arrives once for all of its own
+  if (parts == 1 && a.seqs > 1) last_sequence(gridDim.x);
 }
 
 // Sums of other ranks or micro-batches added: one CTA, a warp per sequence.
