@@ -313,7 +313,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   h->chunks = static_cast<int>((n + chunk - 1) / chunk);
 
   cudaError_t e = cudaGetDevice(&h->device);
-  if (e == cudaSuccess) e = lmoe::ns_small_plan(R, C, &h->small_ctas, &h->small_width);
+  if (e == cudaSuccess) e = lmoe::ns_small_plan(B, R, C, &h->small_ctas, &h->small_width);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e != cudaSuccess) {

@@ -63,7 +63,8 @@ struct NsSmallArgs {
 // Whether the one-launch kernel takes matrices of this size (short side at most
 // 128, long side at most 4096): *ctas CTAs a matrix and *width columns of its
 // long side a CTA, or *ctas = 0.
-cudaError_t ns_small_plan(long long rows, long long cols, int* ctas, int* width);
+cudaError_t ns_small_plan(long long batch, long long rows, long long cols, int* ctas,
+                          int* width);
 cudaError_t launch_ns_small(const NsSmallArgs& a, long long batch, cudaStream_t s);
 
 }  // namespace lmoe

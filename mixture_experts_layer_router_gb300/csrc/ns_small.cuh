@@ -18,9 +18,9 @@
 // tail. What bounds it is latency: five steps of three short products each with
 // its hand-over, 2.5 us a step for one CTA, 5 to 9 us with the exchange of partial
 // grams over a cluster; as tiles of the general kernel the same phases take 20 us a
-// step, because each goes through global memory. Measured: 64 x 2048 31 us (general
-// kernel 117), 128 x 128 22, 128 x 256 28, 128 x 4096 52, 64 matrices of 128 x 256
-// 29, 16 of 100 x 500 45 us. Rows that are no whole vectors go through shared
+// step, because each goes through global memory. Measured: 64 x 2048 28 us (general
+// kernel 83), 128 x 128 22, 128 x 256 28, 128 x 4096 52, 64 matrices of 128 x 256
+// 29, 64 of 128 x 512 54, 16 of 100 x 500 45 us. Rows that are no whole vectors go through shared
 // memory (read as they lie, 100 x 500 took 54 us).
 //
 // Every thread runs through every barrier whatever happened: a wait that gave up
