@@ -121,13 +121,18 @@ long long tiles(long long M, long long N, int shape) {
 
 // Into how many parts gram's k-blocks are split: a few tiles with a long K (the
 // gradient of a router or a projection to a small latent) would leave most SMs
-// idle. A part has 8 k-blocks or more, because joining the parts (through L2)
-// costs about as much as 12.
+// idle. Joining the parts, through L2, costs about as much as 12 k-blocks, so a
+// part has 8 or more and the split has to save more than those: 64 x 8704 (136
+// k-blocks, 8 parts) 253 -> 110 us, 200 x 2000 (32, 4 parts) 118 -> 104, but 1024 x
+// 1024 (16) in two parts 146 -> 158.
+constexpr int kJoinBlocks = 12;
 int gram_split(long long batch, long long side, int k_gram, int sms, int shape) {
   if (shape == lmoe::kNsPair) return 1;
   const long long free_sms = sms / (batch * sym_tiles(side, shape));
-  const long long most = free_sms < k_gram / 8 ? free_sms : k_gram / 8;
-  return static_cast<int>(most < 1 ? 1 : most > 8 ? 8 : most);
+  long long split = free_sms < k_gram / 8 ? free_sms : k_gram / 8;
+  if (split > 8) split = 8;
+  if (split < 2 || (k_gram + split - 1) / split + kJoinBlocks >= k_gram) return 1;
+  return static_cast<int>(split);
 }
 
 // Rounds of tiles decide the shape: a round takes its k-blocks and, once a phase,
@@ -143,7 +148,7 @@ int pick_shape(const latentmoe_muon* h) {
   const auto cost = [&](int shape, long long units, long long block, long long hand_over) {
     const long long sym = (sym_tiles(h->side, shape) * h->batch + units - 1) / units;
     const int split = gram_split(h->batch, h->side, a.k_gram, h->sms, shape);
-    const long long gram = (a.k_gram + split - 1) / split + (split > 1 ? 12 : 0);
+    const long long gram = (a.k_gram + split - 1) / split + (split > 1 ? kJoinBlocks : 0);
     const long long app = (tiles(h->rows, h->cols, shape) * h->batch + units - 1) / units;
     return (sym * (gram + a.k_side) + app * a.k_side) * block + 3 * hand_over;
   };
