@@ -469,3 +469,15 @@ def test_outputs_of_another_stream_do_not_take_memory_in_use():
     for key in want:
         assert torch.equal(got[key], want[key]), key
     assert torch.equal(d, grad) and rel(loss, want["loss"].double()) <= L_TOL
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(300, 16, 2), (4096, 64, 4), (1000, 255, 7), (512, 512, 16)])
+def test_gradient_over_the_logits(T, E, k, renorm):
+    h = layer(E, k, T, renorm)
+    logits, idx, valid, dg = inputs(T, E, k, T + E, pad=True)
+    st = h.balance_loss(logits, idx, valid=valid, balance_coef=BC, z_coef=ZC)
+    args = dict(d_gates=dg, valid=valid, balance_coef=BC, z_coef=ZC)
+    want = h.router_backward(logits, idx, st["counts"], st["tokens"], **args)
+    h.router_backward(logits, idx, st["counts"], st["tokens"], out=logits, **args)
+    assert torch.equal(logits, want)
