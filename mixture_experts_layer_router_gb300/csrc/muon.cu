@@ -135,6 +135,17 @@ int gram_split(long long batch, long long side, int k_gram, int sms, int shape) 
   return static_cast<int>(split);
 }
 
+// apply takes the tiles that hold the first three quarters of A's rows first, so
+// that the SMs that its last round leaves idle can begin with the gram tiles of
+// those rows. Without / with, in turn: 4096 x 8704 2095 / 2005 us, 8704 x 4096 2227 /
+// 2168, 4096 x 4096 1155 / 1136, 6 of 640 x 640 154 / 148; one or two quarters first
+// gain less (4096 x 8704 1 % and nothing), stacks of many matrices take the same
+// time either way.
+long long apply_cut(long long side) {
+  const long long cut = side * 3 / 4 / 256 * 256;  // whole tiles of every shape
+  return cut > 0 ? cut : side;
+}
+
 // Rounds of tiles decide the shape: a round takes its k-blocks and, once a phase,
 // the hand-over of the results to the next phase. In ns, measured: a k-block 270
 // (narrow), 320 (single), 310 (pair): an SM takes in about 64 bytes a clock, which
@@ -203,6 +214,11 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
   a.sym_tiles = static_cast<int>(sym_tiles(h->side, shape));
   a.m_tiles = static_cast<int>((h->rows + bm - 1) / bm);
   a.apply_tiles = static_cast<int>(tiles(h->rows, h->cols, shape));
+  const long long cut = apply_cut(h->side);
+  a.cut = static_cast<int>(cut);
+  a.lower = static_cast<int>(cut == h->side ? a.apply_tiles
+                             : h->tall      ? cut / lmoe::ns_bn(shape) * a.m_tiles
+                                            : cut / bm * (a.apply_tiles / a.m_tiles));
   a.split = gram_split(h->batch, h->side, a.k_gram, h->sms, shape);
   a.group = h->group;
   a.out_mode = out_mode;
@@ -339,7 +355,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   const size_t o_dp = take(static_cast<size_t>(B) * lda * 4);
   // the parts of a split gram product, in either shape that may be asked for
   size_t parts = 0;
-  a.done_ld = 3 * h->steps;
+  a.done_ld = 4 * h->steps;
   for (int shape : {lmoe::kNsSingle, lmoe::kNsNarrow}) {
     const long long split = gram_split(B, side, a.k_gram, h->sms, shape);
     if (split == 1) continue;
@@ -347,7 +363,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
     const size_t need = static_cast<size_t>(B * n_tiles * split) * lmoe::ns_bm(shape) *
                         lmoe::ns_bn(shape) * 4;
     if (need > parts) parts = need;
-    const long long ld = 3 * h->steps + n_tiles * lmoe::kNsEpiWarps;
+    const long long ld = 4 * h->steps + n_tiles * lmoe::kNsEpiWarps;
     if (ld > a.done_ld) a.done_ld = static_cast<int>(ld);
   }
   const size_t o_parts = take(parts);

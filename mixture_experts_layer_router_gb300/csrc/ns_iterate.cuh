@@ -39,11 +39,14 @@
 // One launch instead of three a step: the tiles of all phases form one sequence
 // that running CTAs take from a counter (groups of matrices; in a group: steps,
 // phases, matrices, tiles), and a tile waits until every tile of its matrix's
-// preceding phase has been stored (a count per matrix and phase). While one
-// matrix waits, tiles of the others run. Progress: tiles are taken in sequence order by running
-// CTAs alone and wait only for earlier ones, so the earliest unfinished tile can
-// always proceed. No buffer is overwritten early: a phase's inputs were read by
-// phases that its own predecessor has waited for.
+// preceding phase has been stored (a count per matrix and phase; apply has two, for
+// the rows of A below a cut, whose tiles come first, and for the others, and a gram
+// tile below the cut waits for the first alone). While one matrix waits, tiles of
+// the others run. Progress: tiles are taken in sequence order by running CTAs alone
+// and wait only for earlier ones, so the earliest unfinished tile can always
+// proceed. No buffer is overwritten early: a phase's inputs were read by phases that
+// its own predecessor has waited for (gram writes A and its diagonal, which no apply
+// reads; poly waits for all of gram, and with that for all of the apply before).
 //
 // Tiles (NsShape):
 //   pair    256 x 256 on two SMs (cta_group::2, each CTA holds 128 rows of A and
@@ -65,7 +68,7 @@
 // through L2 at 13 TB/s in all; 8 x 1024 x 2048: 392 us, 575 MB read
 // and 578 MB written in DRAM, tensor pipe busy 36 % of the time; 64 x 2048 x 1024:
 // 2.82 ms, 0.85 PFLOP/s of the 2.41 TFLOP that the symmetric form needs;
-// 4096 x 8704 with the step around it: 2.17 ms, 1.17 PFLOP/s. Single
+// 4096 x 8704 2.0 ms, 1.26 PFLOP/s. Single
 // and narrow: the hand-over between phases (4 to 5 us: last store, count, first
 // load, ring, epilogue) and the 64 bytes a clock that an SM takes in:
 // 3 x 777 x 1333 213 us, 1024 x 1024 147 us, 512 x 512 103 us.
@@ -151,13 +154,15 @@ struct NsArgs {
   int rows, cols, side, tall, steps;
   int sym_tiles;       // of gram and poly
   int m_tiles, apply_tiles;
+  int cut, lower;      // rows of A up to which apply goes first, and its tiles for them
   int k_gram, k_side;  // k-blocks of gram, of poly and apply
   int split;           // parts of gram's k-blocks, each a tile of its own
   long long ld_x, ld_a;
   float* diag_a;       // [batch, ld_a]
   float* diag_p;
   float* parts;        // [batch, sym_tiles, split, tile] gram's partial sums (split > 1)
-  int* done;           // a matrix: [3 steps] epilogue warps that have stored, then
+  int* done;           // a matrix: [4 steps] epilogue warps that have stored gram, poly
+                       // and the lower and upper part of apply, then
                        // [sym_tiles, kNsEpiWarps] warps that have left partial sums
   int done_ld;
   int* counter;        // next tile of the sequence
@@ -223,6 +228,7 @@ struct NsTile {
   int step, phase;
   int row0, col0;  // of the result
   bool mirror;     // symmetric result, tile below the diagonal
+  bool upper;      // apply: past the cut
   int tile, part;  // gram: of the matrix, of its k-blocks
   int kb0, kbs;    // first k-block and how many
 };
@@ -264,6 +270,7 @@ __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
     c.kbs = (c.part + 1) * a.k_gram / split - c.kb0;
   }
   c.tile = local;
+  c.upper = false;
   constexpr int BM = ns_bm(SHAPE), BN = ns_bn(SHAPE);
   constexpr int R = BM / BN;  // tiles across a square of the diagonal
   int i, j;
@@ -276,8 +283,16 @@ __device__ __forceinline__ NsTile ns_decode(int t, const NsArgs& a) {
     j = local - R * (i * (i + 1) / 2);
     c.mirror = j < R * i;
   } else {
-    j = local / a.m_tiles;
-    i = local - j * a.m_tiles;
+    c.upper = local >= a.lower;
+    int m = a.m_tiles, i0 = 0;
+    if (!a.tall) {
+      const int low = (a.cut + BM - 1) / BM;
+      if (c.upper) local -= a.lower;
+      i0 = c.upper ? low : 0;
+      m = c.upper ? m - low : low;
+    }
+    j = local / m;
+    i = i0 + local - j * m;
     c.mirror = false;
   }
   c.row0 = i * BM;
@@ -597,13 +612,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     if constexpr (PAIR) tc_commit_pair(bar, 0x3);
     else tc_commit(bar);
   };
-  // One thread: until every tile of the phase before this one of the same
-  // matrix has been stored (acquire; bounded).
-  auto wait_phase = [&](const NsTile& c) {
-    if (c.step == 0 && c.phase == kNsGram) return true;
-    const int before = 3 * c.step + c.phase - 1;
-    const int* p = a.done + static_cast<long long>(c.b) * a.done_ld + before;
-    const int want = kStores * (c.phase == kNsGram ? a.apply_tiles : a.sym_tiles);
+  // One thread: until `want` warps have arrived at a count (acquire; bounded).
+  auto wait_count = [&](const int* p, int want) {
     if (ld_acquire_gpu(p) >= want) return true;
     const uint64_t t0 = global_timer_ns();
     uint32_t n = 0;
@@ -621,6 +631,15 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
       }
     }
+  };
+  // One thread: until every tile of the phase before this one of the same
+  // matrix that this one reads has been stored.
+  auto wait_phase = [&](const NsTile& c) {
+    const int* p = a.done + static_cast<long long>(c.b) * a.done_ld + 4 * c.step + c.phase - 1;
+    if (c.phase != kNsGram) return wait_count(p, kStores * a.sym_tiles);
+    if (c.step == 0) return true;
+    if (!wait_count(p - 1, kStores * a.lower)) return false;
+    return c.row0 < a.cut || wait_count(p, kStores * (a.apply_tiles - a.lower));
   };
 
   if (threadIdx.x == 0) {
@@ -901,7 +920,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           __syncwarp();
           if (lane == 0) {
             __threadfence();
-            const int n = atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 3 * a.steps +
+            const int n = atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 4 * a.steps +
                                         c.tile * kNsEpiWarps + (warp - 2),
                                     1);
             __threadfence();
@@ -1034,7 +1053,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         if (lane == 0) {
           bulk_wait_all();
           __threadfence();
-          atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 3 * c.step + c.phase, 1);
+          atomicAdd(a.done + static_cast<long long>(c.b) * a.done_ld + 4 * c.step + c.phase +
+                        (c.upper ? 1 : 0),
+                    1);
         }
       }
       if (++acc == 2) {
