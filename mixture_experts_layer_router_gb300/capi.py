@@ -345,14 +345,16 @@ class LatentMoE:
         return ps, cn
 
     def _rows(self, t, name: str, T: int):
-        """Row stride of a [T, E] fp32 tensor whose columns are contiguous."""
+        """Row stride of a [T, E] fp32 tensor whose columns are contiguous and whose
+        rows do not overlap (a stride of 0, an expanded row, means E to the library)."""
         import torch
         E = self.dims.num_experts
+        ld = t.stride(0) if T > 1 and t.dim() == 2 else E
         if not (t.dtype is torch.float32 and t.is_cuda and t.shape == (T, E) and
-                (E == 1 or t.stride(1) == 1)):
+                (E == 1 or t.stride(1) == 1) and ld >= E):
             raise ValueError(f"{name} must be a float32 CUDA tensor [{T}, {E}] with contiguous "
-                             "rows")
-        return t.stride(0) if T > 1 else E
+                             "rows that do not overlap")
+        return ld
 
     def _per_slot(self, t, name: str, T: int, dtype) -> None:
         if not (t.dtype is dtype and t.is_cuda and t.shape == (T, self.k) and t.is_contiguous()):

@@ -69,3 +69,41 @@ def test_binding_refuses_coefficient_lists(lib):
         capi.Muon(8, 8, steps=5, coefs=[(1.0, 0.0, 0.0)] * 4)
     with pytest.raises(ValueError):
         capi.Muon(8, 8, steps=5, coefs=(1.0, 2.0))
+
+
+class _Device:
+    """A tensor as the binding sees one on the GPU: attributes and strides, no data."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda = t, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("T,E", [(2, 1), (7, 16), (64, 13)])
+def test_binding_refuses_rows_that_overlap(lib, T, E):
+    """Expanded rows (stride 0, which the C entries read as E) and rows closer than E
+    are refused before anything is launched; one row may have any stride."""
+    import torch
+    layer = object.__new__(capi.LatentMoE)
+    layer.dims, layer.k, layer.handle = capi.latentmoe_dims(128, 128, E, 128, 0, T), 1, None
+    idx = _Device(torch.zeros((T, 1), dtype=torch.int32))
+    counts, tokens = _Device(torch.zeros((1, E), dtype=torch.int32)), _Device(
+        torch.zeros(1, dtype=torch.int32))
+    good = _Device(torch.zeros((T, E)))
+    wide = _Device(torch.zeros((T, E + 3))[:, :E])
+    assert layer._rows(good, "logits", T) == E
+    assert layer._rows(wide, "logits", T) == E + 3
+    one = torch.zeros((1, E))
+    assert layer._rows(_Device(one.expand(1, E)), "logits", 1) == E
+    bad = [_Device(one.expand(T, E))]
+    if E > 1:
+        bad.append(_Device(torch.zeros(T * E).as_strided((T, E), (E - 1, 1))))
+    for x in bad:
+        with pytest.raises(ValueError):
+            layer.balance_loss(x, idx)
+        with pytest.raises(ValueError):
+            layer.router_backward(x, idx, counts, tokens)
+        with pytest.raises(ValueError):
+            layer.router_backward(good, idx, counts, tokens, out=x)
