@@ -125,11 +125,12 @@ __device__ __forceinline__ void reduce_row(float (&v)[V], Op op) {
   }
 }
 
-// Exponentials as powers of two: exp(x - max) = 2^(c x - top) with c = log2 e and
-// top = c max rounded once, which is one fused multiply-add and one special
-// function. The rounding of top is common to a row and cancels in p; in lse =
-// max + log2(sum) / c it is at most 2^-24 of |max|. The special functions are the
-// hardware's (2 ulp): errors of p and lse stay below 4e-6.
+// Exponentials as powers of two: exp(x - max) = 2^(c (x - max)), c = log2 e. The
+// difference comes first: as one fused multiply-add, 2^(c x - fl(c max)), the rounding
+// of c max would stay in the exponent, harmless for ordinary logits (it is common to
+// the row) but beyond fp32 from |max| of about 1e9 on, where masks of -1e10 or -1e30
+// are. The special functions are the hardware's (2 ulp): errors of p stay below 5e-6
+// for x within 32 of max, those of lse below 1e-6 + 2^-24 |max|.
 constexpr float kLog2E = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
 __device__ __forceinline__ float pow2(float x) {
@@ -137,14 +138,13 @@ __device__ __forceinline__ float pow2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp_of(float m, float x) { return pow2((x - m) * kLog2E); }
 __device__ __forceinline__ float recip(float x) { return __fdividef(1.0f, x); }
 
 // The maxima of a batch's rows (0 for a row of -inf alone).
 template <class R>
 struct Tops {
-  float max[R::U], top[R::U];
-  bool big;  // of the whole warp: some c max would overflow (a row masked with
-             // the type's lowest value); then the difference is taken first
+  float max[R::U];
   __device__ __forceinline__ explicit Tops(const float (&x)[R::U][R::N]) {
 #pragma unroll
     for (int u = 0; u < R::U; ++u) {
@@ -154,30 +154,16 @@ struct Tops {
       max[u] = m;
     }
     reduce_row<R::LANES>(max, Max());
-    bool far = false;
 #pragma unroll
-    for (int u = 0; u < R::U; ++u) {
+    for (int u = 0; u < R::U; ++u)
       if (max[u] == -INFINITY) max[u] = 0.0f;
-      top[u] = max[u] * kLog2E;
-      far |= fabsf(max[u]) > 1e37f;
-    }
-    big = __any_sync(0xffffffffu, far) != 0;
-  }
-  // exp(x - m), m the maximum of a row of the warp, rounded as in exp_row
-  __device__ __forceinline__ float exp_of(float m, float x) const {
-    return big ? pow2((x - m) * kLog2E) : pow2(fmaf(x, kLog2E, -(m * kLog2E)));
   }
   // x <- exp(x - max); the lane's part of the sum. A row of -inf alone sums to 0,
   // a NaN makes its row's sum NaN.
   __device__ __forceinline__ float exp_row(int u, float (&x)[R::N]) const {
     float s = 0.0f, s2 = 0.0f;
-    if (big) {
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) x[i] = pow2((x[i] - max[u]) * kLog2E);
-    } else {
-#pragma unroll
-      for (int i = 0; i < R::N; ++i) x[i] = pow2(fmaf(x[i], kLog2E, -top[u]));
-    }
+    for (int i = 0; i < R::N; ++i) x[i] = exp_of(max[u], x[i]);
 #pragma unroll
     for (int i = 0; i < R::N; i += 2) {
       s += x[i];
@@ -667,14 +653,14 @@ __global__ void __launch_bounds__(kBackThreads)
         if (a.renorm) {
           float own = ch.reduce(cur.xi[p], Max());
           if (own == -INFINITY) own = 0.0f;
-          if (has) g = pow2((cur.xi[p] - own) * kLog2E);
+          if (has) g = exp_of(own, cur.xi[p]);
           const float gs = ch.reduce(g, Add());
           const float gd = ch.reduce(g * cur.dg[p], Add());
           const float ginv = gs == 0.0f ? 0.0f : recip(gs);
           term = g * ginv * (cur.dg[p] - gd * ginv);
         } else {
           const float2 st = row < R::BATCH ? stat[row] : make_float2(0.0f, 0.0f);
-          if (has) g = tops.exp_of(st.x, cur.xi[p]) * st.y;
+          if (has) g = exp_of(st.x, cur.xi[p]) * st.y;
           term = g * cur.dg[p];
           const float gd = ch.reduce(term, Add());
           __syncwarp();
@@ -708,34 +694,34 @@ __global__ void __launch_bounds__(kBackThreads)
       const bool on = in && cur.valid[u] != 0 && sum[u] != 0.0f;
       float shift = on ? fmaf(zq, tops.lse(u, sum[u]), -dot[u] * inv[u]) : 0.0f;
       if (GATES && !a.renorm) shift -= stat[u * R::ROWS + sub].x;
-      // a token that does not count gets zeros (whatever its logits hold) or
-      // the gates' part alone
+      // With e_e = p_e / inv as e_e (wt_e inv + shift inv): two multiply-adds an element,
+      // the gates' terms included. A token that does not count gets no loss's part.
+      const bool dense = GATES || on;
+      const float wi = on ? inv[u] : 0.0f, si = shift * inv[u];
+      float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
       float d[R::N];
 #pragma unroll
-      for (int i = 0; i < R::N; ++i) {
-        const float v = (cur.x[u][i] * inv[u]) * (on ? wt[i] + shift : shift);
-        d[i] = GATES || on ? v : 0.0f;
-      }
-      if constexpr (GATES) {
-        float* mine = sparse + (u * R::ROWS + sub) * R::WIDTH;
-        if constexpr (R::VEC) {
+      for (int v = 0; v < R::NV; ++v) {
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (GATES && R::VEC) {
+          float4* at = reinterpret_cast<float4*>(mine + 4 * (q + R::LANES * v));
+          const float4 o = *at;
+          *at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          f[0] = o.x;
+          f[1] = o.y;
+          f[2] = o.z;
+          f[3] = o.w;
+        } else if constexpr (GATES) {
 #pragma unroll
-          for (int v = 0; v < R::NV; ++v) {
-            float4* at = reinterpret_cast<float4*>(mine + 4 * (q + R::LANES * v));
-            const float4 f = *at;
-            *at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            d[4 * v] += f.x;
-            d[4 * v + 1] += f.y;
-            d[4 * v + 2] += f.z;
-            d[4 * v + 3] += f.w;
+          for (int i = 0; i < 4; ++i) {
+            f[i] = mine[R::col(q, 4 * v + i)];
+            mine[R::col(q, 4 * v + i)] = 0.0f;
           }
-        } else {
+        }
 #pragma unroll
-          for (int i = 0; i < R::N; ++i) {
-            const int c = R::col(q, i);
-            d[i] += mine[c];
-            mine[c] = 0.0f;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float e = cur.x[u][4 * v + i];
+          d[4 * v + i] = dense ? fmaf(e, fmaf(wt[4 * v + i], wi, si), f[i]) : f[i];
         }
       }
       if (in) {
