@@ -317,6 +317,8 @@ int latentmoe_lbl_stats(latentmoe_t h, float* prob_sum, int32_t* counts,
  *   balance = 1/S sum_s E/(k N_s^2) sum_e counts[s,e] prob_sum[s,e]
  *   z       = 1/S sum_s z_sum[s] / N_s          (terms with N_s = 0 are 0)
  *   loss    = {balance_coef balance + z_coef z, balance, z}
+ * (z is infinite where an lse^2 is beyond fp32; with z_coef = 0 loss[0] is
+ * balance_coef balance even so.)
  * Every array is fp32 or int32 on the device. NaN logits of a counting token
  * make the loss NaN. Expert ids outside [0, E) are not counted and set
  * LATENTMOE_STATUS_BAD_EXPERT. */

@@ -210,9 +210,11 @@ __device__ __forceinline__ bool arrive_last(unsigned* ticket, unsigned n, int* f
   return *flag != 0;
 }
 
+// Without its coefficient z is no part of the loss: the square of an lse beyond 1.8e19
+// is infinite, and 0 times that no number.
 __device__ __forceinline__ void store_loss(float* loss, float balance, float z, float bc,
                                            float zc) {
-  loss[0] = bc * balance + zc * z;
+  loss[0] = zc != 0.0f ? bc * balance + zc * z : bc * balance;
   loss[1] = balance;
   loss[2] = z;
 }

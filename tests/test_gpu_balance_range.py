@@ -90,3 +90,27 @@ def test_large_logits_with_the_z_term(E, k):
     q = 2 * ZC / T * lse[:, None]
     dot = (p * w).sum(1, keepdim=True)
     check_gradient(out, p * (w - dot + q), p * (w + dot + q.abs()))
+
+
+@pytest.mark.parametrize("E,k", [(64, 4), (13, 3)])
+def test_no_z_term_without_its_coefficient(E, k):
+    """A row whose lse squared overflows: z is infinite, and with z_coef = 0 it is no
+    part of the loss."""
+    T = 32
+    h = layer(E, k, T)
+    logits, idx, _, _ = inputs(T, E, k, 7)
+    logits[3] = torch.finfo(torch.float32).min
+    for seq_len in (0, 8):
+        got = h.balance_loss(logits, idx, seq_len=seq_len, balance_coef=0.5, z_coef=0.0)
+        assert bool(torch.isinf(got["z_sum"]).any()) and bool(torch.isinf(got["loss"][2]))
+        assert bool(torch.isfinite(got["loss"][1]))
+        assert torch.equal(got["loss"][0], 0.5 * got["loss"][1])
+        again = h.balance_loss_from_stats(got, balance_coef=0.5, z_coef=0.0)
+        assert bool(torch.isinf(again[2]))
+        assert torch.equal(again[0], 0.5 * again[1])
+        on = h.balance_loss(logits, idx, seq_len=seq_len, balance_coef=0.5, z_coef=1e-3)
+        assert bool(torch.isinf(on["loss"][0]))
+    # NaN stays NaN with either coefficient at zero
+    logits[5, 1] = float("nan")
+    for bc, zc in ((0.5, 0.0), (0.0, 0.5), (0.0, 0.0)):
+        assert bool(torch.isnan(h.balance_loss(logits, idx, balance_coef=bc, z_coef=zc)["loss"][0]))
