@@ -354,7 +354,9 @@ int latentmoe_balance_loss_from_stats(latentmoe_t h, const latentmoe_balance_sta
  * d_gates fp32 [T, k] or NULL for the loss alone (idx may then be NULL too).
  * counts [S, E] and tokens [S] are the forward's, or sums over ranks and
  * micro-batches (the counts carry no gradient). The loss's part is zero for
- * tokens that do not count; the gates' part is given for every token. Ids
+ * tokens that do not count; the gates' part is given for every token, and is
+ * zero where all d_gates of the token are: padding with zero d_gates may hold
+ * NaN or infinite logits. Ids
  * outside [0, E) contribute nothing; repeated ids of a token add up. d_logits
  * [T, E] fp32 with row stride ldd (0: E) is written whole, and may be logits
  * itself where ldd = ld. One launch; asynchronous; deterministic. Errors as

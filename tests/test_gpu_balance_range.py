@@ -114,3 +114,61 @@ def test_no_z_term_without_its_coefficient(E, k):
     logits[5, 1] = float("nan")
     for bc, zc in ((0.5, 0.0), (0.0, 0.5), (0.0, 0.0)):
         assert bool(torch.isnan(h.balance_loss(logits, idx, balance_coef=bc, z_coef=zc)["loss"][0]))
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(16, 2), (64, 4), (61, 4), (13, 3), (256, 7), (512, 16), (8, 1)])
+def test_padding_may_hold_anything_beside_gates(E, k, renorm):
+    """Padded tokens whose gates carry no gradient get zeros whatever their logits
+    hold, and leave the other tokens' gradients as they are, bit for bit."""
+    T = 90
+    h = layer(E, k, T, renorm)
+    logits, idx, _, dg = inputs(T, E, k, 13)
+    pad = torch.arange(T, device="cuda") % 3 == 1
+    valid = (~pad).to(torch.uint8)
+    dg[pad] = 0.0
+    st = h.balance_loss(logits, idx, valid=valid, balance_coef=BC, z_coef=ZC)
+    args = dict(d_gates=dg, valid=valid, balance_coef=BC, z_coef=ZC)
+    clean = h.router_backward(logits, idx, st["counts"], st["tokens"], **args)
+    assert not bool(clean[pad].any()) and bool(clean[~pad].any())
+    inf, nan = float("inf"), float("nan")
+    dirty = logits.clone()
+    rows = pad.nonzero().flatten().tolist()
+    fills = [nan, inf, -inf, torch.finfo(torch.float32).max, torch.finfo(torch.float32).min]
+    for i, r in enumerate(rows):
+        if i % 3 == 0:
+            dirty[r] = fills[i // 3 % len(fills)]            # the whole row
+        elif i % 3 == 1:
+            dirty[r, idx[r, 0].long()] = fills[i // 3 % 2]   # a chosen expert
+        else:
+            dirty[r, (idx[r, 0].long() + 1) % E] = fills[i // 3 % 2]
+    again = h.balance_loss(dirty, idx, valid=valid, balance_coef=BC, z_coef=ZC)
+    for key in st:
+        assert torch.equal(st[key], again[key]), key
+    got = h.router_backward(dirty, idx, st["counts"], st["tokens"], **args)
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("E,k", [(64, 4), (13, 3), (512, 8)])
+def test_gates_of_padding_with_nan_elsewhere(E, k):
+    """Renormalised gates depend on the chosen logits alone: a NaN beside them in a
+    padded token does not reach their gradient. Plain gates hold every logit, and the
+    NaN is not hidden."""
+    T = 40
+    logits, idx, _, dg = inputs(T, E, k, 19)
+    valid = torch.ones(T, dtype=torch.uint8, device="cuda")
+    valid[::2] = 0
+    other = torch.ones((T, E), dtype=torch.bool, device="cuda").scatter_(1, idx.long(), False)
+    spot = other.to(torch.int32).argmax(1)  # the first expert that was not chosen
+    dirty = logits.clone()
+    dirty[::2] = dirty[::2].scatter(1, spot[::2, None], float("nan"))
+    for renorm in (True, False):
+        h = layer(E, k, T, renorm)
+        st = h.balance_loss(logits, idx, valid=valid)
+        clean = h.router_backward(logits, idx, st["counts"], st["tokens"], d_gates=dg, valid=valid)
+        got = h.router_backward(dirty, idx, st["counts"], st["tokens"], d_gates=dg, valid=valid)
+        if renorm:
+            assert torch.equal(got, clean)
+        else:
+            assert torch.equal(got[1::2], clean[1::2])
+            assert bool(torch.isnan(got[::2]).any(1).all())
