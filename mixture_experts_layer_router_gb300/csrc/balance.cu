@@ -544,7 +544,7 @@ struct BackRows {
       valid[u] = in && a.valid != nullptr ? a.valid[t0 + r] : 1;
     }
   }
-  // after load: the choices' logits (ids outside [0, E): none)
+  // after load: the choices' logits (ids outside [0, E): none, and no gradient)
   __device__ __forceinline__ void gather(const RouterBackwardArgs& a, long long t0, int base,
                                          const Choices<R>& ch) {
     if constexpr (GATES) {
@@ -552,7 +552,10 @@ struct BackRows {
       for (int p = 0; p < ROUNDS; ++p) {
         if (p >= ch.rounds) break;
         const bool has = static_cast<unsigned>(id[p]) < static_cast<unsigned>(a.E);
-        if (!has) id[p] = -1;
+        if (!has) {  // its gradient, which may be anything, with it
+          id[p] = -1;
+          dg[p] = 0.0f;
+        }
         xi[p] = has ? a.logits[(t0 + base + ch.row(p)) * a.ld + id[p]] : -INFINITY;
       }
     }

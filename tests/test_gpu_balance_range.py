@@ -8,6 +8,8 @@ G_TOL of the sum of the absolute values of a gradient entry's terms.
 import pytest
 import torch
 
+from mixture_experts_layer_router_gb300 import capi
+
 from test_gpu_balance_loss import BC, G_TOL, P_TOL, ZC, inputs, layer, rel
 
 pytestmark = pytest.mark.gpu
@@ -172,3 +174,25 @@ def test_gates_of_padding_with_nan_elsewhere(E, k):
         else:
             assert torch.equal(got[1::2], clean[1::2])
             assert bool(torch.isnan(got[::2]).any(1).all())
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(16, 2), (61, 4), (512, 16)])
+def test_gradients_of_dropped_slots_are_not_read(E, k, renorm):
+    """A slot whose id is outside [0, E) contributes nothing, whatever its d_gates hold."""
+    T = 33
+    h = layer(E, k, T, renorm)
+    logits, idx, _, dg = inputs(T, E, k, 29)
+    idx[::3, 0] = -1
+    idx[1::3, k - 1] = E
+    st = h.balance_loss(logits, idx, balance_coef=BC)
+    assert h.status() == capi.STATUS_BAD_EXPERT
+    dropped = (idx < 0) | (idx >= E)
+    args = dict(balance_coef=BC)
+    want = h.router_backward(logits, idx, st["counts"], st["tokens"],
+                             d_gates=dg.masked_fill(dropped, 0.0), **args)
+    assert bool(torch.isfinite(want).all())
+    for v in (5.0, float("inf"), float("nan")):
+        got = h.router_backward(logits, idx, st["counts"], st["tokens"],
+                                d_gates=dg.masked_fill(dropped, v), **args)
+        assert torch.equal(got, want), v
