@@ -525,8 +525,9 @@ const char* latentmoe_strerror(int code);
  * the momentum are fp32. The result is within about 2e-3 of its norm of the
  * exact iteration's, its rounding to bf16 included. A matrix of zeros gives
  * zeros; a NaN or an infinity makes its own matrix NaN, not the others. The
- * squared norm is held in fp32 (norms below 1.8e19). Results are bitwise
- * reproducible. */
+ * squared norm is held in fp32: right for norms below 1.8e19 and down to the
+ * smallest eps (entries whose squares are no fp32 numbers are scaled first),
+ * and a matrix of a larger norm gives zeros. Results are bitwise reproducible. */
 typedef struct latentmoe_muon* latentmoe_muon_t;
 
 enum { LATENTMOE_BF16 = 0, LATENTMOE_FP32 = 1 }; /* element types of g and w below */

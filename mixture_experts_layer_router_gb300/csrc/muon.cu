@@ -205,7 +205,7 @@ int iterate(latentmoe_muon* h, const lmoe::NsUpdate& u, int out_mode, void* out,
     h->launches += 1;
     return LATENTMOE_OK;
   }
-  NS_CK(h, lmoe::launch_ns_norm(u, h->batch, n, h->chunks, h->chunk, h->partial, s));
+  NS_CK(h, lmoe::launch_ns_norm(u, h->batch, n, h->chunks, h->chunk, h->eps, h->partial, s));
   NS_CK(h, lmoe::launch_ns_init(u, h->batch, h->rows, h->cols, a.ld_x, h->chunks, h->partial,
                                 h->eps, h->scale0, h->x32, h->x16, a.done, a.done_ld, a.counter, s));
   h->launches += 2;
@@ -368,7 +368,7 @@ int latentmoe_muon_create(const latentmoe_muon_dims* dims, latentmoe_muon_t* out
   }
   const size_t o_parts = take(parts);
   const size_t o_done = take(static_cast<size_t>(B) * a.done_ld * 4), o_counter = take(16);
-  const size_t o_partial = take(static_cast<size_t>(B) * h->chunks * 4), o_status = take(16);
+  const size_t o_partial = take(static_cast<size_t>(B) * h->chunks * 8), o_status = take(16);
   e = cudaMalloc(&h->ws, off);
   if (e != cudaSuccess) {
     cudaGetLastError();

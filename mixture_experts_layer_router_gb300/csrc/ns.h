@@ -10,7 +10,8 @@ namespace lmoe {
 
 // Update U of each matrix from gradient and momentum, and the partial sums of
 // its squares: partial[b * chunks + c] over chunk c of matrix b (n elements a
-// matrix). momentum null: U = G. One launch.
+// matrix), with an eps below kNsPlainEps those of the tiny entries in the batch *
+// chunks floats after them. momentum null: U = G. One launch.
 constexpr int kNsMaxChunks = 1024;
 constexpr int kNsNormThreads = 256;
 struct NsUpdate {
@@ -21,7 +22,7 @@ struct NsUpdate {
   bool nesterov;
 };
 cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int chunks,
-                           long long chunk, float* partial, cudaStream_t s);
+                           long long chunk, float eps, float* partial, cudaStream_t s);
 
 // X_0 = U / (|U|_F + eps) times `scale` in fp32 and in fp16, [batch,
 // rows, ld]; the padding columns are zero. U is formed as by launch_ns_norm from

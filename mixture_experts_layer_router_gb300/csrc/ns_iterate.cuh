@@ -223,6 +223,37 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t p
   return done != 0;
 }
 
+// Sum of squares for the Frobenius norm, added up in fp32. Squares below 2^-126 lose
+// bits and those below 2^-149 are gone, which for n elements takes at most sqrt(n 2^-149)
+// from the norm, 2.6e-18 at the largest size: nothing beside an eps of 1e-12. Below
+// that, entries under 2^-40 are added apart, times 2^80, so that norms down to the
+// smallest eps are right. (A matrix of ordinary entries has the same sum either way.)
+constexpr float kNsPlainEps = 1e-12f;
+struct NsSquares {
+  static constexpr float kTiny = 9.094947017729282e-13f;  // 2^-40
+  static constexpr float kUp = 1.2089258196146292e24f;    // 2^80
+  static constexpr float kDown = 8.271806125530277e-25f;  // 2^-80
+  float sum = 0.0f, tiny = 0.0f;
+  template <int V>
+  __device__ __forceinline__ void add(const float (&v)[V], bool apart) {
+    if (apart) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool low = fabsf(v[j]) < kTiny;
+        const float t = low ? v[j] * kUp : 0.0f, x = low ? 0.0f : v[j];
+        tiny = fmaf(t, t, tiny);
+        sum = fmaf(x, x, sum);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum = fmaf(v[j], v[j], sum);
+    }
+  }
+  __device__ __forceinline__ float norm() const {
+    return sum == 0.0f ? sqrtf(tiny) * kDown : sqrtf(fmaf(tiny * kDown, kDown, sum));
+  }
+};
+
 struct NsTile {
   int b;           // matrix
   int step, phase;

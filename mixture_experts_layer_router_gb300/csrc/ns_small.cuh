@@ -36,7 +36,7 @@ constexpr int kSmallX = 128 * kSmallW * 2;   // 64 KB: tiles of 128 rows x 64 co
 constexpr int kSmallA = 128 * 128 * 2;       // 32 KB: A', and P
 constexpr int kSmallPart = 128 * 128 * 4;    // 64 KB: partial gram
 constexpr int kSmallBytes = 1024 + kSmallX + 2 * kSmallA + kSmallPart + 128 * 4 * 2 +
-                            kSmallCluster * 4 + 8 * 4 + 64;
+                            kSmallCluster * 8 + 8 * 8 + 64;
 static_assert(kSmallBytes <= 232448, "Newton-Schulz small kernel shared memory");
 
 __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -196,9 +196,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   uint8_t* part = pop + kSmallA;
   float* diag = reinterpret_cast<float*>(part + kSmallPart);  // d of A, then of P
   float* diag_p = diag + 128;
-  float* norms = diag_p + 128;                                // [kSmallCluster]
-  float* warp_sum = norms + kSmallCluster;                    // [8]
-  uint64_t* bar = reinterpret_cast<uint64_t*>(warp_sum + 8);
+  float* norms = diag_p + 128;                                // [2][kSmallCluster]
+  float* warp_sum = norms + 2 * kSmallCluster;                // [2][8]
+  uint64_t* bar = reinterpret_cast<uint64_t*>(warp_sum + 16);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 
   // ---- the update U, its norm
   const long long base = static_cast<long long>(b) * a.rows * a.cols;
-  float sum = 0.0f;
+  NsSquares sq;
   for (int ch = half; ch < chunks; ch += 2) {
     const int j0 = col0 + ch * 32;
     float v[32];
@@ -273,15 +273,31 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     uint32_t r[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      sum = fmaf(v[k], v[k], sum);
+      sq.sum = fmaf(v[k], v[k], sq.sum);
       r[k] = __float_as_uint(v[k]);
     }
     tmem_st_32cols(t_x + static_cast<uint32_t>(32 * ch), r);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) warp_sum[warp] = sum;
   tmem_st_wait();
+  const bool apart = a.eps < kNsPlainEps;
+  if (apart) {  // the squares again, from tensor memory
+    sq.sum = 0.0f;
+    for (int ch = half; ch < chunks; ch += 2) {
+      uint32_t r[32];
+      float v[32];
+      tmem_ld_32cols(t_x + static_cast<uint32_t>(32 * ch), r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+      sq.add(v, true);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq.tiny += __shfl_xor_sync(0xffffffffu, sq.tiny, o);
+    if (lane == 0) warp_sum[8 + warp] = sq.tiny;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sq.sum += __shfl_xor_sync(0xffffffffu, sq.sum, o);
+  if (lane == 0) warp_sum[warp] = sq.sum;
   __syncthreads();
   // every CTA of the cluster has started: its shared memory may be written
   cluster_sync();
@@ -289,12 +305,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     float t = 0.0f;
     for (int w = 0; w < 8; ++w) t += warp_sum[w];
     st_cluster_f32(mapa_shared(smem_addr(&norms[rank]), threadIdx.x), t);
+    if (apart) {
+      t = 0.0f;
+      for (int w = 8; w < 16; ++w) t += warp_sum[w];
+      st_cluster_f32(mapa_shared(smem_addr(&norms[kSmallCluster + rank]), threadIdx.x), t);
+    }
   }
   __syncwarp();
   cluster_sync();
-  float total = 0.0f;
-  for (int r = 0; r < a.ctas; ++r) total += norms[r];
-  const float inv = 1.0f / (sqrtf(total) + a.eps);
+  NsSquares all;
+  for (int r = 0; r < a.ctas; ++r) all.sum += norms[r];
+  if (apart)
+    for (int r = 0; r < a.ctas; ++r) all.tiny += norms[kSmallCluster + r];
+  const float inv = 1.0f / (all.norm() + a.eps);
   for (int ch = half; ch < chunks; ch += 2) {
     uint32_t r[32];
     tmem_ld_32cols(t_x + static_cast<uint32_t>(32 * ch), r);

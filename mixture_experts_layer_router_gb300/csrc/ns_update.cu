@@ -12,7 +12,7 @@
 // with bf16 g and fp32 m 22 us for 168 MB (norm: g and m read, m written; DRAM 64 %
 // busy) and 32 us for 201 MB (init: 61 %).
 // U is formed with separately rounded products and sums, so that the momentum
-// equals m.mul_(mu).add_(g) bit for bit. The sum of squares is held in fp32:
+// equals m.mul_(mu).add_(g) bit for bit. The sum of squares is held in fp32 (NsSquares):
 // a matrix whose norm reaches 1.8e19 has an infinite sum, and X_0 = 0.
 #include "kernels.h"
 #include "ns.h"
@@ -77,13 +77,14 @@ __device__ __forceinline__ float block_sum(float v) {
 template <bool F32, int V>
 __global__ void __launch_bounds__(kNsNormThreads)
     ns_norm_kernel(const void* g, float* mom, float mu, int nesterov,
-                   long long n, long long chunk, float* partial) {
+                   long long n, long long chunk, float eps, float* partial) {
   pdl_wait();
   pdl_launch_dependents();
   const long long base = static_cast<long long>(blockIdx.y) * n;
   const long long lo = blockIdx.x * chunk;
   const long long hi = lo + chunk < n ? lo + chunk : n;
-  float sum = 0.0f;
+  const bool apart = eps < kNsPlainEps;
+  NsSquares sq;
   for (long long i = lo + static_cast<long long>(threadIdx.x) * V; i < hi;
        i += static_cast<long long>(kNsNormThreads) * V) {
     float v[V];
@@ -107,11 +108,16 @@ __global__ void __launch_bounds__(kNsNormThreads)
         for (int j = 0; j < V; ++j) p[j] = m[j];
       }
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum = fmaf(v[j], v[j], sum);
+    sq.add(v, apart);
   }
-  const float t = block_sum(sum);
-  if (threadIdx.x == 0) partial[static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x] = t;
+  const float t = block_sum(sq.sum);
+  const long long at = static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (threadIdx.x == 0) partial[at] = t;
+  if (apart) {
+    __syncthreads();
+    const float tiny = block_sum(sq.tiny);
+    if (threadIdx.x == 0) partial[static_cast<long long>(gridDim.y) * gridDim.x + at] = tiny;
+  }
 }
 
 template <bool F32, bool VEC>
@@ -127,9 +133,16 @@ __global__ void __launch_bounds__(kNsNormThreads)
     for (int i = threadIdx.x; i < phases; i += kNsNormThreads) done[b * phases + i] = 0;
     if (b == 0 && threadIdx.x == 0) *counter = 0;
   }
-  float s = 0.0f;
-  for (int c = threadIdx.x; c < chunks; c += kNsNormThreads) s += partial[b * chunks + c];
-  const float inv = 1.0f / (sqrtf(block_sum(s)) + eps);
+  NsSquares sq;
+  for (int c = threadIdx.x; c < chunks; c += kNsNormThreads) sq.sum += partial[b * chunks + c];
+  sq.sum = block_sum(sq.sum);
+  if (eps < kNsPlainEps) {
+    const float* apart = partial + static_cast<long long>(gridDim.y) * chunks + b * chunks;
+    for (int c = threadIdx.x; c < chunks; c += kNsNormThreads) sq.tiny += apart[c];
+    __syncthreads();
+    sq.tiny = block_sum(sq.tiny);
+  }
+  const float inv = 1.0f / (sq.norm() + eps);
   const long long base = b * rows * cols;
   const long long per_row = ld / 4;
   const long long total = rows * per_row;
@@ -173,7 +186,7 @@ __global__ void __launch_bounds__(kNsNormThreads)
 }
 
 cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int chunks,
-                           long long chunk, float* partial, cudaStream_t s) {
+                           long long chunk, float eps, float* partial, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(batch));
   const dim3 block(kNsNormThreads);
   const int nes = u.nesterov ? 1 : 0;
@@ -181,13 +194,13 @@ cudaError_t launch_ns_norm(const NsUpdate& u, long long batch, long long n, int 
   const bool vec = n % 8 == 0;
   if (u.g_f32)
     return vec ? launch_kernel(ns_norm_kernel<true, 8>, grid, block, 0, s, 1, false, u.g,
-                               u.momentum, u.mu, nes, n, chunk, partial)
+                               u.momentum, u.mu, nes, n, chunk, eps, partial)
                : launch_kernel(ns_norm_kernel<true, 1>, grid, block, 0, s, 1, false, u.g,
-                               u.momentum, u.mu, nes, n, chunk, partial);
+                               u.momentum, u.mu, nes, n, chunk, eps, partial);
   return vec ? launch_kernel(ns_norm_kernel<false, 8>, grid, block, 0, s, 1, false, u.g,
-                             u.momentum, u.mu, nes, n, chunk, partial)
+                             u.momentum, u.mu, nes, n, chunk, eps, partial)
              : launch_kernel(ns_norm_kernel<false, 1>, grid, block, 0, s, 1, false, u.g,
-                             u.momentum, u.mu, nes, n, chunk, partial);
+                             u.momentum, u.mu, nes, n, chunk, eps, partial);
 }
 
 cudaError_t launch_ns_init(const NsUpdate& u, long long batch, long long rows, long long cols,

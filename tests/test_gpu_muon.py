@@ -326,3 +326,27 @@ def test_output_of_another_stream_does_not_take_memory_in_use():
     o = m.orthogonalize(g, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 100, 304), (2, 300, 104), (2, 128, 512), (1, 33, 131),
+                                             (2, 304, 200), (1, 200, 333), (1, 333, 201)])
+def test_small_updates_with_a_small_eps(batch, rows, cols, dt):
+    """The smallest eps that is taken, and updates whose squares are no fp32 numbers."""
+    gh.lib()
+    m = capi.Muon(rows, cols, batch=batch, eps=1e-30)
+    x = rand((batch, rows, cols), 37)
+    few = torch.zeros_like(x)
+    few[:, ::7, ::5] = 1e13  # some entries far above the others
+    for g in (x * 1e-18, x * 1e-20, x * 1e-22, x * 1e-24, x * 1e-28, x * 1e-31, x * 1e-34,
+              x * 1e-24 + few * x * 1e-24, x):
+        g = g.to(dt)
+        assert rel(m.orthogonalize(g), newton_schulz(g, eps=1e-30)) <= TOL
+    w, mo = torch.zeros_like(x), torch.zeros_like(x)
+    g = (x * 1e-24).to(dt)
+    m.step(w, g, mo, lr=1.0, momentum_coef=0.5, nesterov=True)
+    want = -newton_schulz(g.double() * 1.5, eps=1e-30)
+    assert rel(w, want) <= TOL
+    zero = torch.zeros_like(g)
+    assert torch.equal(m.orthogonalize(zero), torch.zeros_like(x, dtype=torch.bfloat16))
+    assert m.status() == 0
