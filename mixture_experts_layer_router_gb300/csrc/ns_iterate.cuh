@@ -923,6 +923,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        // lane 0 has acquired the count for the warp: a shuffle orders no memory
+        __syncwarp();
         if (row + lane < M && (poly || !a.tall)) by_row = __ldcg(diag + row + lane);
         if (!sym) by_row = fmaf(f.d_x, by_row, f.a_x);
         load_col(0);
@@ -959,6 +961,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           }
           mine = __shfl_sync(0xffffffffu, last_in, 0) != 0;
           if (!mine) break;
+          __syncwarp();  // the other lanes' reads come after lane 0's fence
         }
         for (int i = 0; i < chunks; ++i) {
           const int col = col0 + 64 * i;
