@@ -523,7 +523,9 @@ const char* latentmoe_strerror(int code);
  * the neighbourhood of 1, its singular vectors stay. Products of fp16
  * operands with power-of-two scales and fp32 accumulation; X, the norms and
  * the momentum are fp32. The result is within about 2e-3 of its norm of the
- * exact iteration's, its rounding to bf16 included. A matrix of zeros gives
+ * exact iteration's, its rounding to bf16 included; fp32 weights take X without
+ * that rounding, within about 1e-3 (a step of a 4096 x 8704 matrix leaves them
+ * 7.1e-7 of their norm off, fp32 operands 4.6e-8). A matrix of zeros gives
  * zeros; a NaN or an infinity makes its own matrix NaN, not the others. The
  * squared norm is held in fp32: right for norms below 1.8e19 and down to the
  * smallest eps (entries whose squares are no fp32 numbers are scaled first),

@@ -22,12 +22,12 @@
 // All sums over tokens are fp32 in a fixed order: lanes, warps, CTAs, groups
 // of CTAs (integers may be added in any order).
 //
-// Measured (device time, inputs in L2 or, for the last, larger than it):
+// Measured (device time, inputs in turn: the last two larger than L2 together):
 //                          loss                 backward with the gates' part
-//   128 x 16, top-2        3.9 us
-//   4096 x 64, top-4       8.7 us               3.4 us
-//   16384 x 512, top-8    13.3 us (2.6 TB/s)   14 us (4.9 TB/s)
-//   16 x 4096 x 256       21.1 us (3.3 TB/s)   25.7 us (5.4 TB/s, copy: 6.7)
+//   128 x 16, top-2        3.8 us
+//   4096 x 64, top-4       8.5 us               3.4 us
+//   16384 x 512, top-8    14.2 us (2.4 TB/s)   14.6 us (4.7 TB/s)
+//   16 x 4096 x 256       20.7 us (3.3 TB/s)   25.9 us (5.3 TB/s, copy: 6.7)
 // The loss: launch and one warp's chain, then two levels of sums over the CTAs (4
 // us in all) and 16 warps an SM that issue about 0.6 instructions a cycle and
 // scheduler; 24 or 32 warps leave too few registers for the rows in flight (slower).

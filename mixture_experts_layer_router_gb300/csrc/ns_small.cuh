@@ -20,7 +20,7 @@
 // grams over a cluster; as tiles of the general kernel the same phases take 20 us a
 // step, because each goes through global memory. Measured: 64 x 2048 28 us (general
 // kernel 83), 128 x 128 22, 128 x 256 28, 128 x 4096 52, 64 matrices of 128 x 256
-// 29, 64 of 128 x 512 54, 16 of 100 x 500 45 us. Rows that are no whole vectors go through shared
+// 29, 64 of 128 x 512 54, 16 of 100 x 500 42 us. Rows that are no whole vectors go through shared
 // memory (read as they lie, 100 x 500 took 54 us).
 //
 // Every thread runs through every barrier whatever happened: a wait that gave up

@@ -10,7 +10,7 @@
 // every block (the result does not depend on scheduling), forms U again and
 // writes X_0 in fp32 and fp16. Both are bound by memory traffic: 8 x 1024 x 2048
 // with bf16 g and fp32 m 22 us for 168 MB (norm: g and m read, m written; DRAM 64 %
-// busy) and 32 us for 201 MB (init: 61 %).
+// busy) and 32 to 36 us for 201 MB (init: 61 to 55 %).
 // U is formed with separately rounded products and sums, so that the momentum
 // equals m.mul_(mu).add_(g) bit for bit. The sum of squares is held in fp32 (NsSquares):
 // a matrix whose norm reaches 1.8e19 has an infinite sum, and X_0 = 0.
