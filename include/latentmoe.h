@@ -18,7 +18,9 @@
  * balance loss with per-expert counts (latentmoe_balance_loss), the gradient
  * of that loss and of the gates with respect to the logits
  * (latentmoe_router_backward), and orthogonalised matrix updates
- * (latentmoe_muon_*).
+ * (latentmoe_muon_*); for the block around it, the RMS norm with the residual's
+ * addition and its gradient (latentmoe_rms_norm*), and the global gradient norm
+ * with clipping (latentmoe_grad_*).
  *
  * Conventions for every entry point:
  * - Return 0 (LATENTMOE_OK) on success, a negative LATENTMOE_ERR_* otherwise.
@@ -601,6 +603,115 @@ int latentmoe_muon_get_status(latentmoe_muon_t h, uint32_t* device_status);
 int latentmoe_muon_get_launch_count(latentmoe_muon_t h, int64_t* launches);
 int latentmoe_muon_last_cuda_error(latentmoe_muon_t h);
 int latentmoe_muon_destroy(latentmoe_muon_t h);
+
+/* ---- RMS norm with the residual's addition. ------------------------------
+ * What stands between a residual stream and the layer (or the gated block
+ * below), and its gradient. The pages give no formula; it is the usual one. For
+ * T tokens of width d:
+ *
+ *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd weight
+ *
+ * All in fp32; y and rstd come from the sum before its rounding to the residual's
+ * type. Types are LATENTMOE_BF16 or LATENTMOE_FP32; an fp32 x takes an fp32
+ * residual. Rows may be strided (ld in elements, codes in bytes; 0: d) and begin
+ * at any address that their type allows; 16-byte aligned rows with d % 8 == 0 are
+ * read in wide accesses.
+ * codes: y in E4M3, written beside y or alone. scale_block 0: a scale a token,
+ * scales [T]; 128: one for every 128 channels, scales [T, ceil(d / 128)], the last
+ * block of a row maybe shorter. As latentmoe_quantize_e4m3: scale = max|y| / 448 (1
+ * for zeros, at least 2^-126), code = E4M3(y * (1/scale)), saturating; a NaN is the
+ * NaN code and does not move the scale. */
+typedef struct {
+  const void* x;
+  const void* residual; /* NULL: none */
+  const void* weight;   /* [d] */
+  void* sum;            /* s in the residual's type; NULL: not stored; may be residual */
+  void* y;              /* NULL: codes alone; may be x, of the same type and ld */
+  uint8_t* codes;       /* NULL: none */
+  float* scales;
+  float* rstd;          /* [T], for the gradient; NULL: not stored */
+  int64_t ld_x, ld_residual, ld_sum, ld_y, ld_codes;
+  int32_t x_dtype, residual_dtype, weight_dtype, y_dtype;
+  int32_t scale_block;
+  float eps;            /* >= 1e-30 */
+} latentmoe_norm;
+
+/* One launch, asynchronous on `stream`, on the current device; no handle, no
+ * scratch, bitwise reproducible, capturable. T >= 1, 1 <= d <= 16384. Rows of
+ * numbers beyond 1.8e19, whose squares fp32 cannot hold, come out right; a NaN
+ * makes its own row NaN. Errors: INVALID_ARG (NULL x or weight, neither y nor
+ * codes, codes without scales, sum without residual, sizes, ld < d, an unknown
+ * type or scale_block, eps), UNSUPPORTED (d > 16384, T >= 2^31, an fp32 x with a
+ * bf16 residual, a pointer not aligned to its type), CUDA. */
+int latentmoe_rms_norm(const latentmoe_norm* n, int64_t T, int64_t d, latentmoe_stream_t stream);
+
+/* The gradient. With a = dy weight and n = s rstd (s as stored, rstd [T] of the
+ * forward):
+ *
+ *   dx = d_sum + rstd (a - n mean(a n)),   dw = sum over tokens of dy n
+ *
+ * dx is the gradient of s, and so of x and of the residual alike; d_sum is the
+ * gradient that reached s on its own way down the stream (NULL: none). s, d_sum and
+ * dx have one type (s_dtype); dx may be s or d_sum, of the same ld. dx16: dx once
+ * more in bf16, for an fp32 stream whose sublayer works in bf16 (NULL: none).
+ * dw: fp32 [d], written whole; NULL: none. */
+typedef struct {
+  const void* dy;
+  const void* s;
+  const void* weight;
+  const float* rstd;
+  const void* d_sum;
+  void* dx;
+  void* dx16;
+  float* dw;
+  int64_t ld_dy, ld_s, ld_d_sum, ld_dx, ld_dx16;
+  int32_t dy_dtype, s_dtype, weight_dtype;
+} latentmoe_norm_grad;
+
+/* Two launches (one without dw), asynchronous on `stream`; the partial sums of dw go
+ * to workspace (device, 16-byte aligned, at least
+ * latentmoe_rms_norm_backward_workspace(T, d) bytes, the caller's until the work has
+ * ended; unused without dw). Bitwise reproducible. Errors as latentmoe_rms_norm; also
+ * INVALID_ARG for a workspace that is missing or too small and for dx16 with a bf16
+ * stream. */
+int latentmoe_rms_norm_backward(const latentmoe_norm_grad* n, int64_t T, int64_t d,
+                                void* workspace, size_t workspace_bytes,
+                                latentmoe_stream_t stream);
+/* 0 for sizes that the entry refuses. */
+size_t latentmoe_rms_norm_backward_workspace(int64_t T, int64_t d);
+
+/* ---- Global norm of many gradients, and clipping by it. ------------------
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   out  = g min(1, max_norm / (norm + eps))
+ * What stands between the backward pass and the optimiser step. Tensors are
+ * contiguous, bf16 or fp32, of any length (0 too) and any alignment of their type.
+ * The sum is right for any finite numbers (64 bits where fp32 cannot hold the
+ * squares). A NaN makes the norm and every gradient NaN; an infinity makes the norm
+ * infinite and the gradients zero, itself NaN. The factor is formed in 64 bits and
+ * rounded to fp32; the product is rounded once. */
+typedef struct {
+  const void* g;
+  void* out;      /* clipping: may be g itself; latentmoe_grad_norm does not use it */
+  int64_t n;      /* elements; g and out may be NULL if 0 */
+  int64_t dtype;  /* LATENTMOE_BF16, LATENTMOE_FP32: of g and out */
+} latentmoe_gradient;
+
+/* norm: device fp32 [1]. workspace: device, 16-byte aligned, at least
+ * latentmoe_grad_workspace(count) bytes, the caller's until the work has ended. The
+ * table (host) is read before the call returns. 2 launches for each 1000 tensors, and
+ * one more for the norm alone; asynchronous on `stream`, on the current device; bitwise
+ * reproducible for the same sizes and alignments; capturable. Tensors with a factor of
+ * 1 and out = g are left as they are. Errors: INVALID_ARG (NULL, count < 0, n < 0, an
+ * unknown type, max_norm < 0 or NaN, eps < 0 or not finite, a workspace that is missing
+ * or too small, an out that overlaps another tensor's g or out, or its own g in part),
+ * UNSUPPORTED (a pointer not aligned to its type, more than 2^31 tiles of 32 KB),
+ * OUT_OF_MEMORY (host), CUDA. */
+int latentmoe_grad_norm(const latentmoe_gradient* grads, int64_t count, float* norm,
+                        void* workspace, size_t workspace_bytes, latentmoe_stream_t stream);
+int latentmoe_grad_clip(const latentmoe_gradient* grads, int64_t count, double max_norm,
+                        double eps, float* norm, void* workspace, size_t workspace_bytes,
+                        latentmoe_stream_t stream);
+size_t latentmoe_grad_workspace(int64_t count);
 
 /* ---- Debug entry points: the tensor-core GEMM core on its own. ----------
  * C = epilogue(A B^T) for bf16 A [M, K] and B [N', K] (device, row-major).

@@ -31,7 +31,8 @@ SOURCES = ["api.cu", "route.cu", "combine.cu", "gemm_bf16.cu", "gemm_f32.cu",
            "gemm_swiglu.cu", "gemm_scatter.cu", "gemm_scatter8.cu", "gemm_grouped.cu", "gemm_grouped2.cu", "gemm_fused.cu",
            "pack.cu",
            "router.cu", "route_static.cu", "fp8.cu", "multiround.cu",
-           "balance.cu", "muon.cu", "ns_iterate.cu", "ns_small.cu", "ns_update.cu"]
+           "balance.cu", "muon.cu", "ns_iterate.cu", "ns_small.cu", "ns_update.cu",
+           "block.cu", "norm.cu", "norm_backward.cu", "grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

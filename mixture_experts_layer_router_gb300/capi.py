@@ -73,6 +73,25 @@ class latentmoe_muon_update(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class latentmoe_norm(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in
+                ("x", "residual", "weight", "sum", "y", "codes", "scales", "rstd")] + \
+        [(n, _i64) for n in ("ld_x", "ld_residual", "ld_sum", "ld_y", "ld_codes")] + \
+        [(n, ctypes.c_int32) for n in ("x_dtype", "residual_dtype", "weight_dtype", "y_dtype",
+                                       "scale_block")] + [("eps", ctypes.c_float)]
+
+
+class latentmoe_norm_grad(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in
+                ("dy", "s", "weight", "rstd", "d_sum", "dx", "dx16", "dw")] + \
+        [(n, _i64) for n in ("ld_dy", "ld_s", "ld_d_sum", "ld_dx", "ld_dx16")] + \
+        [(n, ctypes.c_int32) for n in ("dy_dtype", "s_dtype", "weight_dtype")]
+
+
+class latentmoe_gradient(ctypes.Structure):
+    _fields_ = [("g", _c_void_p), ("out", _c_void_p), ("n", _i64), ("dtype", _i64)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "latentmoe_create": (ctypes.c_int, [ctypes.POINTER(latentmoe_dims), ctypes.c_int,
@@ -145,6 +164,16 @@ SIGNATURES = {
     "latentmoe_muon_get_launch_count": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
     "latentmoe_muon_last_cuda_error": (ctypes.c_int, [_c_void_p]),
     "latentmoe_muon_destroy": (ctypes.c_int, [_c_void_p]),
+    "latentmoe_rms_norm": (ctypes.c_int, [ctypes.POINTER(latentmoe_norm), _i64, _i64,
+                                          _c_void_p]),
+    "latentmoe_rms_norm_backward": (ctypes.c_int, [ctypes.POINTER(latentmoe_norm_grad), _i64, _i64,
+                                                   _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "latentmoe_rms_norm_backward_workspace": (ctypes.c_size_t, [_i64, _i64]),
+    "latentmoe_grad_norm": (ctypes.c_int, [_c_void_p, _i64, _c_void_p, _c_void_p,
+                                           ctypes.c_size_t, _c_void_p]),
+    "latentmoe_grad_clip": (ctypes.c_int, [_c_void_p, _i64, ctypes.c_double, ctypes.c_double,
+                                           _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "latentmoe_grad_workspace": (ctypes.c_size_t, [_i64]),
     "latentmoe_debug_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "latentmoe_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64,
                                                     ctypes.POINTER(ctypes.c_uint32)]),
@@ -656,6 +685,166 @@ class Muon:
         self._check(load().latentmoe_muon_get_launch_count(self.handle, ctypes.byref(v)),
                     "latentmoe_muon_get_launch_count")
         return v.value
+
+
+def _here(t, name: str) -> None:
+    # device pointers are the current device's: a tensor of another one is refused
+    import torch
+    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(),
+          f"{name} must be on the current CUDA device")
+
+
+def _token_rows(t, name: str, T: int, d: int, dtypes) -> int:
+    """Row stride of a [T, d] tensor whose rows are contiguous and do not overlap."""
+    _here(t, name)
+    _need(t.dtype in dtypes and tuple(t.shape) == (T, d),
+          f"{name} must be [{T}, {d}] of type {' or '.join(str(x) for x in dtypes)}, "
+          f"got {list(t.shape)} {t.dtype}")
+    ld = t.stride(0) if T > 1 else d
+    _need((d == 1 or t.stride(1) == 1) and ld >= d,
+          f"{name} must have contiguous rows that do not overlap")
+    return ld
+
+
+def _norm_weight(weight, d: int) -> int:
+    _here(weight, "weight")
+    _need(tuple(weight.shape) == (d,) and weight.is_contiguous(),
+          f"weight must be a contiguous [{d}]")
+    return _dtype_code(weight, "weight")
+
+
+SCALE_BLOCK = 128  # channels of an E4M3 scale block
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, quantize: Optional[str] = None,
+             keep_y: bool = False, y_dtype=None, out_sum=None, stream=None):
+    """RMS norm of s = x + residual, rows x [T, d] (bf16 or fp32), weight [d]:
+    {"y": [T, d], "rstd": [T] fp32 for rms_norm_backward, "sum": s in the residual's
+    type where one is given}. quantize "token" or "block": y as E4M3 "codes" (uint8
+    [T, d]) with "scales" fp32 [T, 1] or [T, ceil(d / 128)] instead of y, or beside
+    it with keep_y. y has x's type unless y_dtype says otherwise. out_sum: where s
+    goes, e.g. the residual itself."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, rms_norm, x, weight, eps, residual, quantize, keep_y, y_dtype,
+                          out_sum)
+    _need(x.dim() == 2, "x must be [T, d]")
+    _need(quantize in (None, "token", "block"), 'quantize must be None, "token" or "block"')
+    both = (torch.bfloat16, torch.float32)
+    T, d = x.shape
+    a = latentmoe_norm(x=x.data_ptr(), weight=weight.data_ptr(), eps=eps,
+                       ld_x=_token_rows(x, "x", T, d, both), x_dtype=_dtype_code(x, "x"),
+                       weight_dtype=_norm_weight(weight, d))
+    rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
+    a.rstd = rstd.data_ptr()
+    out = {"rstd": rstd}
+    if residual is not None:
+        a.residual, a.residual_dtype = residual.data_ptr(), _dtype_code(residual, "residual")
+        a.ld_residual = _token_rows(residual, "residual", T, d, both)
+        s = torch.empty((T, d), dtype=residual.dtype, device=x.device) if out_sum is None else out_sum
+        a.sum, a.ld_sum = s.data_ptr(), _token_rows(s, "out_sum", T, d, (residual.dtype,))
+        out["sum"] = s
+    else:
+        _need(out_sum is None, "out_sum needs a residual")
+    if quantize is None or keep_y:
+        y = torch.empty((T, d), dtype=y_dtype or x.dtype, device=x.device)
+        a.y, a.ld_y, a.y_dtype = y.data_ptr(), d, _dtype_code(y, "y")
+        out["y"] = y
+    if quantize is not None:
+        a.scale_block = SCALE_BLOCK if quantize == "block" else 0
+        n = -(-d // SCALE_BLOCK) if quantize == "block" else 1
+        out["codes"] = torch.empty((T, d), dtype=torch.uint8, device=x.device)
+        out["scales"] = torch.empty((T, n), dtype=torch.float32, device=x.device)
+        a.codes, a.scales = out["codes"].data_ptr(), out["scales"].data_ptr()
+    check(load().latentmoe_rms_norm(ctypes.byref(a), T, d, _stream(None)), "latentmoe_rms_norm")
+    return out
+
+
+def rms_norm_backward(dy, s, weight, rstd, d_sum=None, dw: bool = True, dx_bf16: bool = False,
+                      stream=None):
+    """Gradient of rms_norm: {"dx": [T, d] of s's type, the gradient of x and of the
+    residual alike, "dw": [d] fp32}. s: the norm's "sum" (its x where there was no
+    residual); d_sum: the gradient that reached it from further down the stream.
+    dx_bf16 (fp32 streams): "dx16" as well, dx in bf16."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, rms_norm_backward, dy, s, weight, rstd, d_sum, dw, dx_bf16)
+    _need(dy.dim() == 2, "dy must be [T, d]")
+    both = (torch.bfloat16, torch.float32)
+    T, d = dy.shape
+    _here(rstd, "rstd")
+    _need(rstd.dtype == torch.float32 and tuple(rstd.shape) == (T,) and rstd.is_contiguous(),
+          f"rstd must be a contiguous float32 [{T}]")
+    a = latentmoe_norm_grad(dy=dy.data_ptr(), s=s.data_ptr(), weight=weight.data_ptr(),
+                            rstd=rstd.data_ptr(), ld_dy=_token_rows(dy, "dy", T, d, both),
+                            ld_s=_token_rows(s, "s", T, d, both), dy_dtype=_dtype_code(dy, "dy"),
+                            s_dtype=_dtype_code(s, "s"), weight_dtype=_norm_weight(weight, d))
+    if d_sum is not None:
+        a.d_sum, a.ld_d_sum = d_sum.data_ptr(), _token_rows(d_sum, "d_sum", T, d, (s.dtype,))
+    out = {"dx": torch.empty((T, d), dtype=s.dtype, device=s.device)}
+    a.dx, a.ld_dx = out["dx"].data_ptr(), d
+    if dx_bf16:
+        _need(s.dtype == torch.float32, "dx_bf16 is for float32 streams")
+        out["dx16"] = torch.empty((T, d), dtype=torch.bfloat16, device=s.device)
+        a.dx16, a.ld_dx16 = out["dx16"].data_ptr(), d
+    ws, size = None, 0
+    if dw:
+        size = load().latentmoe_rms_norm_backward_workspace(T, d)
+        ws = torch.empty((size,), dtype=torch.uint8, device=s.device)
+        out["dw"] = torch.empty((d,), dtype=torch.float32, device=s.device)
+        a.dw = out["dw"].data_ptr()
+    check(load().latentmoe_rms_norm_backward(ctypes.byref(a), T, d, _ptr(ws), size, _stream(None)),
+          "latentmoe_rms_norm_backward")
+    return out
+
+
+def _gradient_table(grads, out):
+    import array
+    import torch
+    grads = list(grads)
+    _need(len(grads) > 0, "no gradients")
+    _need(out is None or len(out) == len(grads), "out must have one tensor for each gradient")
+    bf16, f32, dev = torch.bfloat16, torch.float32, torch.cuda.current_device()
+    flat = array.array("q")
+    for i, g in enumerate(grads):
+        dt = g.dtype
+        _need((dt is bf16 or dt is f32) and g.is_cuda and g.get_device() == dev and
+              g.is_contiguous(),
+              "gradients must be contiguous bfloat16 or float32 tensors on the current CUDA device")
+        to = g
+        if out is not None:
+            to = out[i]
+            _need(to.dtype is dt and to.is_cuda and to.get_device() == dev and
+                  to.is_contiguous() and to.shape == g.shape,
+                  "out must have the gradients' shapes, types and device, and be contiguous")
+        flat.extend((g.data_ptr(), to.data_ptr(), g.numel(), FP32 if dt is f32 else BF16))
+    lib = load()
+    ws = torch.empty((lib.latentmoe_grad_workspace(len(grads)),), dtype=torch.uint8,
+                     device=grads[0].device)
+    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+    return flat, len(grads), norm, ws
+
+
+def gradient_norm(grads, stream=None):
+    """sqrt of the sum of all squares of the tensors (bf16 or fp32), as fp32 [1]."""
+    if stream is not None:
+        return _on_stream(stream, gradient_norm, grads)
+    flat, n, norm, ws = _gradient_table(grads, None)
+    check(load().latentmoe_grad_norm(flat.buffer_info()[0], n, norm.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), _stream(None)), "latentmoe_grad_norm")
+    return norm
+
+
+def clip_gradients(grads, max_norm: float, eps: float = 1e-6, out=None, stream=None):
+    """Scales the tensors by min(1, max_norm / (norm + eps)) in place, or into the
+    tensors of ``out``; returns the norm before it, fp32 [1]."""
+    if stream is not None:
+        return _on_stream(stream, clip_gradients, grads, max_norm, eps, out)
+    flat, n, norm, ws = _gradient_table(grads, out)
+    check(load().latentmoe_grad_clip(flat.buffer_info()[0], n, max_norm, eps, norm.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), _stream(None)),
+          "latentmoe_grad_clip")
+    return norm
 
 
 def stage_name(i: int) -> str:
