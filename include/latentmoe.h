@@ -19,8 +19,9 @@
  * of that loss and of the gates with respect to the logits
  * (latentmoe_router_backward), and orthogonalised matrix updates
  * (latentmoe_muon_*); for the block around it, the RMS norm with the residual's
- * addition and its gradient (latentmoe_rms_norm*), and the global gradient norm
- * with clipping (latentmoe_grad_*).
+ * addition and its gradient (latentmoe_rms_norm*), the shared expert's gated
+ * feed-forward block as an operator with its gradient (latentmoe_ffn_*), and the
+ * global gradient norm with clipping (latentmoe_grad_*).
  *
  * Conventions for every entry point:
  * - Return 0 (LATENTMOE_OK) on success, a negative LATENTMOE_ERR_* otherwise.
@@ -603,6 +604,95 @@ int latentmoe_muon_get_status(latentmoe_muon_t h, uint32_t* device_status);
 int latentmoe_muon_get_launch_count(latentmoe_muon_t h, int64_t* launches);
 int latentmoe_muon_last_cuda_error(latentmoe_muon_t h);
 int latentmoe_muon_destroy(latentmoe_muon_t h);
+
+/* ---- Gated feed-forward block, with its gradient. -------------------------
+ * The shared expert ("MAI-Base-2: Microsoft's 2.8T base model, and whether its
+ * compute numbers add up", section "The model") as an operator of its own on the
+ * caller's weights, for training it and for single tokens:
+ *
+ *   gate = x W_g^T,  up = x W_u^T,  h = SiLU(gate) * up,  y = h W_d^T
+ *
+ * and, from the gate and up that the forward stored,
+ *
+ *   dh = dy W_d,  dg = dh up SiLU'(gate),  du = dh SiLU(gate)
+ *   dx = dg W_g + du W_u,  dW_g = dg^T x,  dW_u = du^T x,  dW_d = dy^T h
+ *
+ * bf16 operands and fp32 accumulators; the activation in fp32, from the
+ * accumulators (forward) or from the stored bf16 gate and up (backward). h, dg and
+ * du are rounded to bf16 between the products. No atomics: results are bitwise
+ * reproducible. Rows of x and dy past T are not read, rows of y and dx past T not
+ * written. */
+typedef struct latentmoe_ffn* latentmoe_ffn_t;
+
+/* hidden d and ffn F: multiples of 8 up to 65536. max_tokens (up to 2^22) bounds T
+ * and sizes the workspace: 2 F max_tokens bytes, 6 F max_tokens with `training`,
+ * which latentmoe_ffn_backward needs. */
+typedef struct {
+  int64_t hidden;
+  int64_t ffn;
+  int64_t max_tokens;
+  int32_t training;
+} latentmoe_ffn_dims;
+
+/* Device bf16, contiguous: w_g, w_u [F, d], w_d [d, F]. Read where they are, at
+ * every call: nothing is copied or laid out anew. */
+typedef struct {
+  const void* w_g;
+  const void* w_u;
+  const void* w_d;
+} latentmoe_ffn_weights;
+
+/* dy, x, dx bf16 [T, d] with row strides (elements, multiples of 8; 0: d); gate and
+ * up bf16 [T, F] contiguous, as the forward stored them. dw_g, dw_u [F, d], dw_d
+ * [d, F] contiguous, bf16 or fp32 (dw_dtype); fp32 ones are added to what is there
+ * with `accumulate`. Any of the four outputs may be NULL, and then what only it needs
+ * (x for dw_g and dw_u; w_g and w_u for dx) may be too. Outputs overlap nothing. */
+typedef struct {
+  const void* dy;
+  const void* x;
+  const void* gate;
+  const void* up;
+  void* dx;
+  void* dw_g;
+  void* dw_u;
+  void* dw_d;
+  int64_t ld_dy, ld_x, ld_dx;
+  int32_t dw_dtype;
+  int32_t accumulate;
+} latentmoe_ffn_grad;
+
+/* Create a handle on the current device and allocate the workspace. The handle
+ * follows the rules of a layer handle: one host thread and one stream at a time (two
+ * captured graphs that use it may not run at once), one device. Errors: INVALID_ARG
+ * (NULL, a size < 1), UNSUPPORTED (beyond the limits above), OUT_OF_MEMORY, CUDA. On
+ * error *out is NULL and nothing stays allocated. */
+int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out);
+
+/* y bf16 [T, d] from x bf16 [T, d] (row strides as above; y may not overlap x); gate
+ * and up bf16 [T, F] contiguous, both or neither NULL. 1 <= T <= max_tokens. 2
+ * launches, asynchronous on `stream`, no host synchronisation; it can be captured into
+ * a CUDA graph once a first call outside the capture has set up the kernels. Errors:
+ * INVALID_ARG, UNSUPPORTED (a pointer that is not 16-byte aligned, a stride that is no
+ * multiple of 8), CUDA. */
+int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, const void* x,
+                          int64_t ld_x, void* y, int64_t ld_y, void* gate, void* up, int64_t T,
+                          latentmoe_stream_t stream);
+
+/* The gradient. Needs a handle made with `training`; otherwise as the forward. Also
+ * UNSUPPORTED: `accumulate` with bf16 gradients. */
+int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
+                           const latentmoe_ffn_grad* g, int64_t T, latentmoe_stream_t stream);
+
+/* Tiles of the products: 0 = 128 x 128 on single SMs, 1 = 256 x 256 on SM pairs, 2
+ * (the default) = whichever is expected to take the least time. */
+int latentmoe_ffn_set_sm_pairs(latentmoe_ffn_t h, int mode);
+
+/* As latentmoe_get_status, latentmoe_get_launch_count, latentmoe_last_cuda_error
+ * and latentmoe_destroy, for a handle of the gated block. */
+int latentmoe_ffn_get_status(latentmoe_ffn_t h, uint32_t* device_status);
+int latentmoe_ffn_get_launch_count(latentmoe_ffn_t h, int64_t* launches);
+int latentmoe_ffn_last_cuda_error(latentmoe_ffn_t h);
+int latentmoe_ffn_destroy(latentmoe_ffn_t h);
 
 /* ---- RMS norm with the residual's addition. ------------------------------
  * What stands between a residual stream and the layer (or the gated block

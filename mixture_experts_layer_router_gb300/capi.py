@@ -73,6 +73,20 @@ class latentmoe_muon_update(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class latentmoe_ffn_dims(ctypes.Structure):
+    _fields_ = [("hidden", _i64), ("ffn", _i64), ("max_tokens", _i64), ("training", ctypes.c_int32)]
+
+
+class latentmoe_ffn_weights(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in ("w_g", "w_u", "w_d")]
+
+
+class latentmoe_ffn_grad(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in ("dy", "x", "gate", "up", "dx", "dw_g", "dw_u", "dw_d")] + \
+        [(n, _i64) for n in ("ld_dy", "ld_x", "ld_dx")] + \
+        [(n, ctypes.c_int32) for n in ("dw_dtype", "accumulate")]
+
+
 class latentmoe_norm(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in
                 ("x", "residual", "weight", "sum", "y", "codes", "scales", "rstd")] + \
@@ -164,6 +178,18 @@ SIGNATURES = {
     "latentmoe_muon_get_launch_count": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
     "latentmoe_muon_last_cuda_error": (ctypes.c_int, [_c_void_p]),
     "latentmoe_muon_destroy": (ctypes.c_int, [_c_void_p]),
+    "latentmoe_ffn_create": (ctypes.c_int, [ctypes.POINTER(latentmoe_ffn_dims),
+                                            ctypes.POINTER(_c_void_p)]),
+    "latentmoe_ffn_forward": (ctypes.c_int, [_c_void_p, ctypes.POINTER(latentmoe_ffn_weights),
+                                             _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                             _i64, _c_void_p]),
+    "latentmoe_ffn_backward": (ctypes.c_int, [_c_void_p, ctypes.POINTER(latentmoe_ffn_weights),
+                                              ctypes.POINTER(latentmoe_ffn_grad), _i64, _c_void_p]),
+    "latentmoe_ffn_set_sm_pairs": (ctypes.c_int, [_c_void_p, ctypes.c_int]),
+    "latentmoe_ffn_get_status": (ctypes.c_int, [_c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
+    "latentmoe_ffn_get_launch_count": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
+    "latentmoe_ffn_last_cuda_error": (ctypes.c_int, [_c_void_p]),
+    "latentmoe_ffn_destroy": (ctypes.c_int, [_c_void_p]),
     "latentmoe_rms_norm": (ctypes.c_int, [ctypes.POINTER(latentmoe_norm), _i64, _i64,
                                           _c_void_p]),
     "latentmoe_rms_norm_backward": (ctypes.c_int, [ctypes.POINTER(latentmoe_norm_grad), _i64, _i64,
@@ -704,6 +730,123 @@ def _token_rows(t, name: str, T: int, d: int, dtypes) -> int:
     _need((d == 1 or t.stride(1) == 1) and ld >= d,
           f"{name} must have contiguous rows that do not overlap")
     return ld
+
+
+class GatedFFN:
+    """A handle on a gated feed-forward block y = (SiLU(x w_g^T) * (x w_u^T)) w_d^T of
+    width ``d`` and hidden width ``F`` (multiples of 8) for up to ``max_tokens`` rows;
+    ``training``: with the gradient's workspace. Weights are the caller's, bf16, and
+    passed at every call: w_g, w_u [F, d], w_d [d, F]."""
+
+    def __init__(self, d: int, F: int, max_tokens: int = 1, training: bool = False):
+        self.dims = latentmoe_ffn_dims(d, F, max_tokens, int(training))
+        h = _c_void_p()
+        check(load().latentmoe_ffn_create(ctypes.byref(self.dims), ctypes.byref(h)),
+              "latentmoe_ffn_create")
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            load().latentmoe_ffn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check(self, code: int, what: str) -> None:
+        if code != OK:
+            raise LatentMoEError(code, what, load().latentmoe_ffn_last_cuda_error(self.handle))
+
+    def _matrix(self, t, name: str, rows: int, cols: int, dtype=None):
+        import torch
+        _here(t, name)
+        if not (t.shape == (rows, cols) and t.dtype is (dtype or torch.bfloat16) and
+                t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype or torch.bfloat16} "
+                             f"[{rows}, {cols}], got {list(t.shape)} {t.dtype}")
+        return t.data_ptr()
+
+    def _weights(self, w_g, w_u, w_d):
+        d, F = self.dims.hidden, self.dims.ffn
+        return latentmoe_ffn_weights(self._matrix(w_g, "w_g", F, d), self._matrix(w_u, "w_u", F, d),
+                                     self._matrix(w_d, "w_d", d, F))
+
+    def forward(self, x, w_g, w_u, w_d, save: bool = False, out=None, stream=None):
+        """y [T, d] bf16 of x [T, d] bf16 (rows may be strided); with ``save`` (y, gate,
+        up), the latter [T, F] bf16 for ``backward``."""
+        import torch
+        if stream is not None:
+            return _on_stream(stream, self.forward, x, w_g, w_u, w_d, save, out)
+        _need(x.dim() == 2, "x must be [T, d]")
+        T, d, F = x.shape[0], self.dims.hidden, self.dims.ffn
+        bf16 = (torch.bfloat16,)
+        ld_x = _token_rows(x, "x", T, d, bf16)
+        y = x.new_empty((T, d)) if out is None else out
+        ld_y = d if out is None else _token_rows(y, "out", T, d, bf16)
+        gate = x.new_empty((T, F)) if save else None
+        up = x.new_empty((T, F)) if save else None
+        self._check(load().latentmoe_ffn_forward(
+            self.handle, ctypes.byref(self._weights(w_g, w_u, w_d)), x.data_ptr(), ld_x,
+            y.data_ptr(), ld_y, _ptr(gate), _ptr(up), T, _stream(None)), "latentmoe_ffn_forward")
+        return (y, gate, up) if save else y
+
+    def backward(self, dy, x, gate, up, w_g, w_u, w_d, dw_dtype=None, out=None,
+                 accumulate: bool = False, need=("dx", "dw_g", "dw_u", "dw_d"), stream=None):
+        """{"dx" [T, d] bf16, "dw_g", "dw_u" [F, d], "dw_d" [d, F]} of dy [T, d]; the
+        weights' gradients are bf16, or dw_dtype=torch.float32. ``out``: a dict of tensors
+        to write to (their type counts), added to with ``accumulate`` (fp32 weights'
+        gradients). ``need``: the ones that are wanted."""
+        import torch
+        if stream is not None:
+            return _on_stream(stream, self.backward, dy, x, gate, up, w_g, w_u, w_d, dw_dtype, out,
+                              accumulate, need)
+        _need(dy.dim() == 2, "dy must be [T, d]")
+        T, d, F = dy.shape[0], self.dims.hidden, self.dims.ffn
+        bf16 = (torch.bfloat16,)
+        out = dict(out or {})
+        names = [n for n in ("dx", "dw_g", "dw_u", "dw_d") if n in need]
+        given = [out[n].dtype for n in names if n != "dx" and n in out]
+        dt = dw_dtype or (given[0] if given else torch.bfloat16)
+        _need(not accumulate or all(n in out for n in names if n != "dx"),
+              "accumulate needs the weights' gradients in out")
+        g = latentmoe_ffn_grad(dy=dy.data_ptr(), ld_dy=_token_rows(dy, "dy", T, d, bf16),
+                               x=x.data_ptr(), ld_x=_token_rows(x, "x", T, d, bf16),
+                               gate=self._matrix(gate, "gate", T, F),
+                               up=self._matrix(up, "up", T, F), accumulate=int(accumulate))
+        got = {}
+        for n in names:
+            if n == "dx":
+                t = out[n] if n in out else dy.new_empty((T, d))
+                g.dx, g.ld_dx = t.data_ptr(), _token_rows(t, n, T, d, bf16)
+            else:
+                shape = (d, F) if n == "dw_d" else (F, d)
+                t = out[n] if n in out else torch.empty(shape, dtype=dt, device=dy.device)
+                g.dw_dtype = _dtype_code(t, n)
+                setattr(g, n, self._matrix(t, n, shape[0], shape[1], dt))
+            got[n] = t
+        self._check(load().latentmoe_ffn_backward(
+            self.handle, ctypes.byref(self._weights(w_g, w_u, w_d)), ctypes.byref(g), T,
+            _stream(None)), "latentmoe_ffn_backward")
+        return got
+
+    def set_sm_pairs(self, mode: int) -> None:
+        """0: 128 x 128 tiles on single SMs; 1: 256 x 256 on SM pairs; 2: automatic."""
+        self._check(load().latentmoe_ffn_set_sm_pairs(self.handle, int(mode)),
+                    "latentmoe_ffn_set_sm_pairs")
+
+    def status(self) -> int:
+        v = ctypes.c_uint32(0)
+        load().latentmoe_ffn_get_status(self.handle, ctypes.byref(v))
+        return v.value
+
+    def launch_count(self) -> int:
+        v = _i64(0)
+        self._check(load().latentmoe_ffn_get_launch_count(self.handle, ctypes.byref(v)),
+                    "latentmoe_ffn_get_launch_count")
+        return v.value
 
 
 def _norm_weight(weight, d: int) -> int:

@@ -1,0 +1,49 @@
+// Launchers of the gated feed-forward block's kernels (internal interface).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lmoe {
+
+// What the epilogue of a launch does with its products' accumulators.
+enum FfnEpi : int {
+  kFfnGateUp = 0,  // B: gate rows and up rows of the same features; h, gate, up
+  kFfnDGate = 1,   // the accumulator is dh; reads gate and up, leaves dg, du, h
+  kFfnPlain = 2    // the product, in bf16 or fp32
+};
+enum FfnShape : int { kFfnSingle = 0, kFfnPair = 1 };
+enum FfnOut : int { kFfnBf16 = 0, kFfnF32 = 1, kFfnF32Add = 2 };
+
+constexpr int kFfnBK = 64;
+__host__ __device__ constexpr int ffn_bm(int shape) { return shape == kFfnPair ? 256 : 128; }
+__host__ __device__ constexpr int ffn_bn(int shape) { return shape == kFfnPair ? 256 : 128; }
+
+// D [M, N] = A B^T summed over `segments` pairs of operands, K each. Operand maps:
+// boxes of 64 x 64 bf16, 128-byte swizzle; (columns, rows) of the matrix in memory.
+// An operand is K-major (rows of M or N, columns of K) or MN-major (rows of K).
+struct alignas(64) FfnProduct {
+  CUtensorMap a[2], b[2];
+  CUtensorMap out[3];  // boxes of 32 x 32: plain: [0]; gate+up: h, gate, up; dgate: dg, du, h
+  int M, N;            // gate+up: N output features
+  int k_blocks;        // of a segment
+  int segments;
+  int a_mn, b_mn;
+  int m_tiles, n_tiles;
+  int first;           // first tile in the launch's sequence
+  int out_mode;        // FfnOut
+  int save;            // gate+up: gate and up are stored
+};
+constexpr int kFfnProducts = 4;
+struct FfnArgs {
+  FfnProduct p[kFfnProducts];
+  CUtensorMap gate, up;  // dgate: boxes of 32 x 32
+  int products;
+  int tiles;
+  int band;  // m-tiles of a band of the raster
+  unsigned* status;
+};
+cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream_t s);
+
+}  // namespace lmoe

@@ -1,4 +1,4 @@
-"""Host-side refusals of the RMS norm and clipping entries (CPU only): addresses that
+"""Host-side refusals of the RMS norm, gated block and clipping entries (CPU only): addresses that
 nothing reads, since every call here is refused before a launch."""
 import ctypes
 import math
@@ -126,3 +126,29 @@ def test_binding_refuses_host_tensors(lib):
         capi.clip_gradients([x], 1.0)
     with pytest.raises(ValueError):
         capi.gradient_norm([])
+
+
+@pytest.mark.parametrize("dims,code", [
+    ((0, 8, 1, 0), INVALID), ((8, 0, 1, 0), INVALID), ((8, 8, 0, 0), INVALID), ((-8, 8, 1, 0), INVALID),
+    ((12, 8, 1, 0), UNSUPPORTED), ((8, 4, 1, 0), UNSUPPORTED), ((65544, 8, 1, 0), UNSUPPORTED),
+    ((8, 1 << 40, 1, 0), UNSUPPORTED), ((8, 8, (1 << 22) + 1, 1), UNSUPPORTED),
+])
+def test_ffn_create_refuses(lib, dims, code):
+    h = ctypes.c_void_p(7)
+    d = capi.latentmoe_ffn_dims(*dims)
+    assert lib.latentmoe_ffn_create(ctypes.byref(d), ctypes.byref(h)) == code
+    assert h.value is None
+
+
+def test_ffn_null(lib):
+    h = ctypes.c_void_p(7)
+    assert lib.latentmoe_ffn_create(None, ctypes.byref(h)) == INVALID
+    assert h.value is None
+    assert lib.latentmoe_ffn_create(ctypes.byref(capi.latentmoe_ffn_dims(8, 8, 1, 0)), None) == INVALID
+    assert lib.latentmoe_ffn_forward(None, None, None, 0, None, 0, None, None, 1, None) == INVALID
+    assert lib.latentmoe_ffn_backward(None, None, None, 1, None) == INVALID
+    assert lib.latentmoe_ffn_set_sm_pairs(None, 0) == INVALID
+    assert lib.latentmoe_ffn_get_status(None, None) == INVALID
+    assert lib.latentmoe_ffn_get_launch_count(None, None) == INVALID
+    assert lib.latentmoe_ffn_last_cuda_error(None) == 0
+    assert lib.latentmoe_ffn_destroy(None) == capi.OK
