@@ -626,7 +626,7 @@ typedef struct latentmoe_ffn* latentmoe_ffn_t;
 
 /* hidden d and ffn F: multiples of 8 up to 65536. max_tokens (up to 2^22) bounds T
  * and sizes the workspace: 2 F max_tokens bytes, 6 F max_tokens with `training`,
- * which latentmoe_ffn_backward needs. */
+ * which latentmoe_ffn_backward needs, and up to 20 MB for the sums of few tokens. */
 typedef struct {
   int64_t hidden;
   int64_t ffn;
@@ -684,7 +684,8 @@ int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
                            const latentmoe_ffn_grad* g, int64_t T, latentmoe_stream_t stream);
 
 /* Tiles of the products: 0 = 128 x 128 on single SMs, 1 = 256 x 256 on SM pairs, 2
- * (the default) = whichever is expected to take the least time. */
+ * (the default) = whichever is expected to take the least time; the forward then has a
+ * kernel of its own for few tokens, which 3 asks for (up to 128 tokens; otherwise as 2). */
 int latentmoe_ffn_set_sm_pairs(latentmoe_ffn_t h, int mode);
 
 /* As latentmoe_get_status, latentmoe_get_launch_count, latentmoe_last_cuda_error

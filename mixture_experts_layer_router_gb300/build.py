@@ -32,7 +32,8 @@ SOURCES = ["api.cu", "route.cu", "combine.cu", "gemm_bf16.cu", "gemm_f32.cu",
            "pack.cu",
            "router.cu", "route_static.cu", "fp8.cu", "multiround.cu",
            "balance.cu", "muon.cu", "ns_iterate.cu", "ns_small.cu", "ns_update.cu",
-           "block.cu", "ffn.cu", "ffn_gemm.cu", "norm.cu", "norm_backward.cu", "grads.cu"]
+           "block.cu", "ffn.cu", "ffn_few.cu", "ffn_gemm.cu",
+           "norm.cu", "norm_backward.cu", "grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -24,12 +24,15 @@ struct latentmoe_ffn {
   bool training = false;
   int device = 0;
   int sms = 1;
-  int mode = 2;  // 0 single, 1 pair, 2 by the expected time
+  int mode = 2;  // 0 single, 1 pair, 2 by the expected time, 3 the kernel for few tokens
   void* ws = nullptr;
   __nv_bfloat16* h = nullptr;   // [max_tokens, F]
   __nv_bfloat16* dg = nullptr;  // training only
   __nv_bfloat16* du = nullptr;
   unsigned* status = nullptr;
+  float* parts = nullptr;   // of the kernel for few tokens
+  int* arrived = nullptr;
+  size_t arrived_bytes = 0;
   int64_t launches = 0;
   int last_cuda = 0;
 };
@@ -54,13 +57,14 @@ int fail(latentmoe_ffn* h, cudaError_t e) {
 
 // 2-D map of a row-major matrix [rows, cols] with row stride ld (elements).
 bool encode(CUtensorMap* map, const void* p, long long rows, long long cols, long long ld, int box,
-            bool f32) {
+            int box_rows, bool f32) {
   const lmoe::EncodeTiledFn fn = lmoe::tensor_map_encoder();
   if (fn == nullptr) return false;
   const int size = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * size};
-  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box)};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box),
+                               static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -74,10 +78,10 @@ struct Mat {
   long long rows, cols, ld;
 };
 bool operand(CUtensorMap* map, const Mat& m) {
-  return encode(map, m.p, m.rows, m.cols, m.ld, 64, false);
+  return encode(map, m.p, m.rows, m.cols, m.ld, 64, 64, false);
 }
 bool chunk(CUtensorMap* map, const Mat& m, bool f32 = false) {
-  return encode(map, m.p, m.rows, m.cols, m.ld, 32, f32);
+  return encode(map, m.p, m.rows, m.cols, m.ld, 32, 32, f32);
 }
 
 // Collects a launch's products; `ok` turns false where a map cannot be made.
@@ -140,13 +144,40 @@ int run(latentmoe_ffn* h, Launch& l, int epi, cudaStream_t s) {
   // ns a k-block, measured for the Newton-Schulz products, whose main loop is the same:
   // single tiles are bound by the 64 bytes a clock that an SM takes in
   int shape = h->mode;
-  if (shape > 1) {
+  if (shape > lmoe::kFfnPair) {
     const double single = 320.0 * plan(l.a, epi, lmoe::kFfnSingle, h->sms);
     const double pair = 310.0 * plan(l.a, epi, lmoe::kFfnPair, h->sms);
     shape = pair <= single ? lmoe::kFfnPair : lmoe::kFfnSingle;
   }
   plan(l.a, epi, shape, h->sms);
   FFN_CK(h, lmoe::launch_ffn(epi, shape, l.a, h->sms, s));
+  h->launches += 1;
+  return LATENTMOE_OK;
+}
+
+// One product for few tokens: out [T, rows] of x [T, K] and weights [rows, K].
+int run_few(latentmoe_ffn* h, int epi, const Mat& x, const void* w0, const void* w1, long long rows,
+            bool early, void* out, long long ld, void* gate, void* up, cudaStream_t s) {
+  const lmoe::PdlScope pdl(true);
+  lmoe::FewArgs a;
+  memset(&a, 0, sizeof(a));
+  a.tokens = static_cast<int>(x.rows);
+  a.rows = static_cast<int>(rows);
+  a.tiles = static_cast<int>(ceil_div(rows, epi == lmoe::kFfnGateUp ? 64 : 128));
+  a.k_blocks = static_cast<int>(ceil_div(x.cols, lmoe::kFfnBK));
+  a.early = early ? 1 : 0;
+  a.parts = h->parts;
+  a.arrived = h->arrived;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.gate = static_cast<__nv_bfloat16*>(gate);
+  a.up = static_cast<__nv_bfloat16*>(up);
+  a.ld = ld;
+  a.status = h->status;
+  const Mat w = {w0, rows, x.cols, x.cols}, v = {w1, rows, x.cols, x.cols};
+  if (!operand(&a.w[0], w) || (w1 != nullptr && !operand(&a.w[1], v)) ||
+      !encode(&a.x, x.p, x.rows, x.cols, x.ld, 64, lmoe::few_tokens(a.tokens), false))
+    return LATENTMOE_ERR_CUDA;
+  FFN_CK(h, lmoe::launch_ffn_few(epi, a, h->sms, s));
   h->launches += 1;
   return LATENTMOE_OK;
 }
@@ -183,7 +214,15 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
     return LATENTMOE_ERR_CUDA;
   }
   const size_t rows = (static_cast<size_t>(p.max_tokens) * p.ffn * 2 + 1023) / 1024 * 1024;
-  const size_t bytes = 1024 + rows * (h->training ? 3 : 1);
+  const long long few = p.max_tokens < lmoe::kFewMost ? p.max_tokens : lmoe::kFewMost;
+  const size_t parts = static_cast<size_t>(h->sms) * 2 * 128 * 4 *
+                       static_cast<size_t>(lmoe::few_tokens(static_cast<int>(few)));
+  const long long tiles = ceil_div(p.ffn, 64) > ceil_div(p.hidden, 128) ? ceil_div(p.ffn, 64)
+                                                                        : ceil_div(p.hidden, 128);
+  // status word and arrival counts, parts, h (dg, du)
+  h->arrived_bytes = static_cast<size_t>(tiles) * 4;
+  const size_t head = (1024 + h->arrived_bytes + 1023) / 1024 * 1024;
+  const size_t bytes = head + parts + rows * (h->training ? 3 : 1);
   e = cudaMalloc(&h->ws, bytes);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -192,12 +231,15 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
   }
   char* base = static_cast<char*>(h->ws);
   h->status = reinterpret_cast<unsigned*>(base);
-  h->h = reinterpret_cast<__nv_bfloat16*>(base + 1024);
+  h->arrived = reinterpret_cast<int*>(base + 1024);
+  h->parts = reinterpret_cast<float*>(base + head);
+  base += head + parts;
+  h->h = reinterpret_cast<__nv_bfloat16*>(base);
   if (h->training) {
-    h->dg = reinterpret_cast<__nv_bfloat16*>(base + 1024 + rows);
-    h->du = reinterpret_cast<__nv_bfloat16*>(base + 1024 + 2 * rows);
+    h->dg = reinterpret_cast<__nv_bfloat16*>(base + rows);
+    h->du = reinterpret_cast<__nv_bfloat16*>(base + 2 * rows);
   }
-  e = cudaMemset(h->status, 0, 1024);
+  e = cudaMemset(h->status, 0, head);
   if (e != cudaSuccess) {
     cudaFree(h->ws);
     delete h;
@@ -229,6 +271,13 @@ int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, con
   FFN_CK(h, cudaSetDevice(h->device));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
   const long long d = h->d, F = h->F;
+  if (T <= lmoe::kFewMost && h->mode >= 2) {
+    const int rc = run_few(h, lmoe::kFfnGateUp, {x, T, d, ld_x}, w->w_g, w->w_u, F, false, h->h, F,
+                           gate, up, s);
+    if (rc != LATENTMOE_OK) return rc;
+    return run_few(h, lmoe::kFfnPlain, {h->h, T, F, F}, w->w_d, nullptr, d, true, y, ld_y, nullptr,
+                   nullptr, s);
+  }
   Launch l(h);
   FfnProduct& p = l.add({x, T, d, ld_x}, false, {w->w_g, F, d, d}, false, T, F, d);
   l.ok = l.ok && operand(&p.b[1], {w->w_u, F, d, d}) && chunk(&p.out[0], {h->h, T, F, F});
@@ -305,7 +354,7 @@ int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
 }
 
 int latentmoe_ffn_set_sm_pairs(latentmoe_ffn_t h, int mode) {
-  if (h == nullptr || mode < 0 || mode > 2) return LATENTMOE_ERR_INVALID_ARG;
+  if (h == nullptr || mode < 0 || mode > 3) return LATENTMOE_ERR_INVALID_ARG;
   h->mode = mode;
   return LATENTMOE_OK;
 }
@@ -317,6 +366,8 @@ int latentmoe_ffn_get_status(latentmoe_ffn_t h, uint32_t* device_status) {
   unsigned v = 0;
   FFN_CK(h, cudaMemcpy(&v, h->status, 4, cudaMemcpyDeviceToHost));
   FFN_CK(h, cudaMemset(h->status, 0, 4));
+  // a launch that gave up may have left arrivals
+  if (v != 0) FFN_CK(h, cudaMemset(h->arrived, 0, h->arrived_bytes));
   *device_status = v;
   if (v & LATENTMOE_STATUS_TIMEOUT) return LATENTMOE_ERR_TIMEOUT;
   return v != 0 ? LATENTMOE_ERR_DEVICE_STATUS : LATENTMOE_OK;

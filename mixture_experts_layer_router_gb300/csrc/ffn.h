@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,7 +24,7 @@ __host__ __device__ constexpr int ffn_bn(int shape) { return shape == kFfnPair ?
 // D [M, N] = A B^T summed over `segments` pairs of operands, K each. Operand maps:
 // boxes of 64 x 64 bf16, 128-byte swizzle; (columns, rows) of the matrix in memory.
 // An operand is K-major (rows of M or N, columns of K) or MN-major (rows of K).
-struct alignas(64) FfnProduct {
+struct FfnProduct {
   CUtensorMap a[2], b[2];
   CUtensorMap out[3];  // boxes of 32 x 32: plain: [0]; gate+up: h, gate, up; dgate: dg, du, h
   int M, N;            // gate+up: N output features
@@ -45,5 +46,31 @@ struct FfnArgs {
   unsigned* status;
 };
 cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream_t s);
+
+// Few tokens: D^T = W x^T with 128 rows of weights by up to 128 tokens a tile
+// (ffn_few.cuh). kFfnGateUp (64 features a tile) or kFfnPlain.
+constexpr int kFewMost = 128;      // tokens
+constexpr int kFewLeast = 8;       // k-blocks of a part, unless a tile has fewer
+struct FewArgs {
+  CUtensorMap w[2];  // gate+up: gate and up; plain: w[0]; boxes of 64 x 64
+  CUtensorMap x;     // [tokens, K]; boxes of 64 columns x few_tokens(tokens) rows
+  int tokens;
+  int rows;          // output features
+  int tiles, k_blocks;
+  int early;         // weights may be loaded before the kernel ahead has finished
+  float* parts;      // [CTAs, 2, few_tokens, 128]
+  int* arrived;      // [tiles], zero; left zero
+  __nv_bfloat16* out;   // h or y, [tokens, ld]
+  __nv_bfloat16* gate;  // or null; [tokens, rows]
+  __nv_bfloat16* up;
+  long long ld;
+  unsigned* status;
+};
+inline int few_tokens(int tokens) {
+  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
+}
+// CTAs of a launch: one an SM, fewer where parts would get too short.
+int few_ctas(int tiles, int k_blocks, int sms);
+cudaError_t launch_ffn_few(int epi, const FewArgs& a, int sms, cudaStream_t s);
 
 }  // namespace lmoe

@@ -75,8 +75,13 @@ SIZES = [(1, 8, 8), (1, 256, 512), (3, 16, 24), (17, 1024, 640), (64, 64, 64), (
          (1000, 128, 1024), (2048, 256, 384)]
 
 
-@pytest.mark.parametrize("mode", [0, 1, 2])
-@pytest.mark.parametrize("T,d,F", SIZES)
+# the kernel for few tokens: borders of its token tiles and of its tiles of weights
+FEW = [(2, 128, 64), (15, 72, 72), (16, 128, 128), (17, 64, 8), (32, 1544, 136), (33, 8, 1000), (64, 2048, 2048),
+       (65, 520, 3000), (127, 136, 264), (128, 4096, 1024), (128, 40, 56), (8, 8704, 512), (1, 8704, 10240)]
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 3])
+@pytest.mark.parametrize("T,d,F", SIZES + FEW)
 def test_forward(T, d, F, mode):
     gh.lib()
     x, w = block(T, d, F, seed=T + d + F)
