@@ -678,8 +678,9 @@ int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, con
                           int64_t ld_x, void* y, int64_t ld_y, void* gate, void* up, int64_t T,
                           latentmoe_stream_t stream);
 
-/* The gradient. Needs a handle made with `training`; otherwise as the forward. Also
- * UNSUPPORTED: `accumulate` with bf16 gradients. */
+/* The gradient, in 2 launches (3 for fewer than 8 tokens). Needs a handle made with
+ * `training`; otherwise as the forward. Also UNSUPPORTED: `accumulate` with bf16
+ * gradients. */
 int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
                            const latentmoe_ffn_grad* g, int64_t T, latentmoe_stream_t stream);
 
@@ -795,7 +796,7 @@ typedef struct {
  * 1 and out = g are left as they are. Errors: INVALID_ARG (NULL, count < 0, n < 0, an
  * unknown type, max_norm < 0 or NaN, eps < 0 or not finite, a workspace that is missing
  * or too small, an out that overlaps another tensor's g or out, or its own g in part),
- * UNSUPPORTED (a pointer not aligned to its type, more than 2^31 tiles of 32 KB),
+ * UNSUPPORTED (a pointer not aligned to its type, more than 2^31 tiles of 64 KB),
  * OUT_OF_MEMORY (host), CUDA. */
 int latentmoe_grad_norm(const latentmoe_gradient* grads, int64_t count, float* norm,
                         void* workspace, size_t workspace_bytes, latentmoe_stream_t stream);

@@ -713,22 +713,34 @@ class Muon:
         return v.value
 
 
+_raw_device = None  # () -> ordinal of the current device
+
+
+def _device() -> int:
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        torch.cuda.current_device()  # CUDA is initialised from here on
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_device()
+
+
 def _here(t, name: str) -> None:
     # device pointers are the current device's: a tensor of another one is refused
-    import torch
-    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(),
-          f"{name} must be on the current CUDA device")
+    if not (t.is_cuda and t.get_device() == _device()):
+        raise ValueError(f"{name} must be on the current CUDA device")
 
 
 def _token_rows(t, name: str, T: int, d: int, dtypes) -> int:
     """Row stride of a [T, d] tensor whose rows are contiguous and do not overlap."""
     _here(t, name)
-    _need(t.dtype in dtypes and tuple(t.shape) == (T, d),
-          f"{name} must be [{T}, {d}] of type {' or '.join(str(x) for x in dtypes)}, "
-          f"got {list(t.shape)} {t.dtype}")
-    ld = t.stride(0) if T > 1 else d
-    _need((d == 1 or t.stride(1) == 1) and ld >= d,
-          f"{name} must have contiguous rows that do not overlap")
+    if t.dtype not in dtypes or t.shape != (T, d):
+        raise ValueError(f"{name} must be [{T}, {d}] of type "
+                         f"{' or '.join(str(x) for x in dtypes)}, got {list(t.shape)} {t.dtype}")
+    step, inner = t.stride()
+    ld = step if T > 1 else d
+    if (inner != 1 and d > 1) or ld < d:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return ld
 
 
@@ -852,8 +864,8 @@ class GatedFFN:
 
 def _norm_weight(weight, d: int) -> int:
     _here(weight, "weight")
-    _need(tuple(weight.shape) == (d,) and weight.is_contiguous(),
-          f"weight must be a contiguous [{d}]")
+    if weight.shape != (d,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{d}]")
     return _dtype_code(weight, "weight")
 
 
@@ -872,35 +884,45 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, quantize: Optional[str
     if stream is not None:
         return _on_stream(stream, rms_norm, x, weight, eps, residual, quantize, keep_y, y_dtype,
                           out_sum)
-    _need(x.dim() == 2, "x must be [T, d]")
-    _need(quantize in (None, "token", "block"), 'quantize must be None, "token" or "block"')
-    both = (torch.bfloat16, torch.float32)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    if quantize not in (None, "token", "block"):
+        raise ValueError('quantize must be None, "token" or "block"')
+    f32 = torch.float32
+    both = (torch.bfloat16, f32)
     T, d = x.shape
-    a = latentmoe_norm(x=x.data_ptr(), weight=weight.data_ptr(), eps=eps,
-                       ld_x=_token_rows(x, "x", T, d, both), x_dtype=_dtype_code(x, "x"),
-                       weight_dtype=_norm_weight(weight, d))
-    rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
-    a.rstd = rstd.data_ptr()
+    ld_x, w_code = _token_rows(x, "x", T, d, both), _norm_weight(weight, d)
+    rstd = x.new_empty(T, dtype=f32)
     out = {"rstd": rstd}
+    r = s = y = codes = scales = None
+    ld_r = ld_s = r_code = y_code = block = 0
     if residual is not None:
-        a.residual, a.residual_dtype = residual.data_ptr(), _dtype_code(residual, "residual")
-        a.ld_residual = _token_rows(residual, "residual", T, d, both)
-        s = torch.empty((T, d), dtype=residual.dtype, device=x.device) if out_sum is None else out_sum
-        a.sum, a.ld_sum = s.data_ptr(), _token_rows(s, "out_sum", T, d, (residual.dtype,))
-        out["sum"] = s
-    else:
-        _need(out_sum is None, "out_sum needs a residual")
+        r, ld_r = residual.data_ptr(), _token_rows(residual, "residual", T, d, both)
+        r_code = FP32 if residual.dtype is f32 else BF16
+        if out_sum is None:
+            s_out, ld_s = residual.new_empty((T, d)), d
+        else:
+            s_out, ld_s = out_sum, _token_rows(out_sum, "out_sum", T, d, (residual.dtype,))
+        out["sum"] = s_out
+        s = s_out.data_ptr()
+    elif out_sum is not None:
+        raise ValueError("out_sum needs a residual")
     if quantize is None or keep_y:
-        y = torch.empty((T, d), dtype=y_dtype or x.dtype, device=x.device)
-        a.y, a.ld_y, a.y_dtype = y.data_ptr(), d, _dtype_code(y, "y")
-        out["y"] = y
+        out["y"] = y_out = x.new_empty((T, d), dtype=y_dtype)
+        y, y_code = y_out.data_ptr(), _dtype_code(y_out, "y")
     if quantize is not None:
-        a.scale_block = SCALE_BLOCK if quantize == "block" else 0
-        n = -(-d // SCALE_BLOCK) if quantize == "block" else 1
-        out["codes"] = torch.empty((T, d), dtype=torch.uint8, device=x.device)
-        out["scales"] = torch.empty((T, n), dtype=torch.float32, device=x.device)
-        a.codes, a.scales = out["codes"].data_ptr(), out["scales"].data_ptr()
-    check(load().latentmoe_rms_norm(ctypes.byref(a), T, d, _stream(None)), "latentmoe_rms_norm")
+        n = 1
+        if quantize == "block":
+            block, n = SCALE_BLOCK, -(-d // SCALE_BLOCK)
+        out["codes"] = x.new_empty((T, d), dtype=torch.uint8)
+        out["scales"] = x.new_empty((T, n), dtype=f32)
+        codes, scales = out["codes"].data_ptr(), out["scales"].data_ptr()
+    a = latentmoe_norm(x.data_ptr(), r, weight.data_ptr(), s, y, codes, scales, rstd.data_ptr(),
+                       ld_x, ld_r, ld_s, d, d, FP32 if x.dtype is f32 else BF16, r_code, w_code,
+                       y_code, block, eps)
+    code = load().latentmoe_rms_norm(ctypes.byref(a), T, d, _stream(None))
+    if code != OK:
+        check(code, "latentmoe_rms_norm")
     return out
 
 
@@ -913,32 +935,39 @@ def rms_norm_backward(dy, s, weight, rstd, d_sum=None, dw: bool = True, dx_bf16:
     import torch
     if stream is not None:
         return _on_stream(stream, rms_norm_backward, dy, s, weight, rstd, d_sum, dw, dx_bf16)
-    _need(dy.dim() == 2, "dy must be [T, d]")
-    both = (torch.bfloat16, torch.float32)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, d]")
+    f32 = torch.float32
+    both = (torch.bfloat16, f32)
     T, d = dy.shape
     _here(rstd, "rstd")
-    _need(rstd.dtype == torch.float32 and tuple(rstd.shape) == (T,) and rstd.is_contiguous(),
-          f"rstd must be a contiguous float32 [{T}]")
-    a = latentmoe_norm_grad(dy=dy.data_ptr(), s=s.data_ptr(), weight=weight.data_ptr(),
-                            rstd=rstd.data_ptr(), ld_dy=_token_rows(dy, "dy", T, d, both),
-                            ld_s=_token_rows(s, "s", T, d, both), dy_dtype=_dtype_code(dy, "dy"),
-                            s_dtype=_dtype_code(s, "s"), weight_dtype=_norm_weight(weight, d))
-    if d_sum is not None:
-        a.d_sum, a.ld_d_sum = d_sum.data_ptr(), _token_rows(d_sum, "d_sum", T, d, (s.dtype,))
-    out = {"dx": torch.empty((T, d), dtype=s.dtype, device=s.device)}
-    a.dx, a.ld_dx = out["dx"].data_ptr(), d
+    if rstd.dtype is not f32 or rstd.shape != (T,) or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be a contiguous float32 [{T}]")
+    ld_dy, ld_s = _token_rows(dy, "dy", T, d, both), _token_rows(s, "s", T, d, both)
+    w_code = _norm_weight(weight, d)
+    ld_ds = 0 if d_sum is None else _token_rows(d_sum, "d_sum", T, d, (s.dtype,))
+    dx = s.new_empty((T, d))
+    out = {"dx": dx}
+    dx16 = ws = grad = None
+    size = 0
     if dx_bf16:
-        _need(s.dtype == torch.float32, "dx_bf16 is for float32 streams")
-        out["dx16"] = torch.empty((T, d), dtype=torch.bfloat16, device=s.device)
-        a.dx16, a.ld_dx16 = out["dx16"].data_ptr(), d
-    ws, size = None, 0
+        if s.dtype is not f32:
+            raise ValueError("dx_bf16 is for float32 streams")
+        out["dx16"] = s.new_empty((T, d), dtype=torch.bfloat16)
+        dx16 = out["dx16"].data_ptr()
+    lib = load()
     if dw:
-        size = load().latentmoe_rms_norm_backward_workspace(T, d)
-        ws = torch.empty((size,), dtype=torch.uint8, device=s.device)
-        out["dw"] = torch.empty((d,), dtype=torch.float32, device=s.device)
-        a.dw = out["dw"].data_ptr()
-    check(load().latentmoe_rms_norm_backward(ctypes.byref(a), T, d, _ptr(ws), size, _stream(None)),
-          "latentmoe_rms_norm_backward")
+        size = lib.latentmoe_rms_norm_backward_workspace(T, d)
+        ws = s.new_empty(size, dtype=torch.uint8)
+        out["dw"] = s.new_empty(d, dtype=f32)
+        grad = out["dw"].data_ptr()
+    a = latentmoe_norm_grad(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+                            _ptr(d_sum), dx.data_ptr(), dx16, grad, ld_dy, ld_s, ld_ds, d, d,
+                            FP32 if dy.dtype is f32 else BF16, FP32 if s.dtype is f32 else BF16,
+                            w_code)
+    code = lib.latentmoe_rms_norm_backward(ctypes.byref(a), T, d, _ptr(ws), size, _stream(None))
+    if code != OK:
+        check(code, "latentmoe_rms_norm_backward")
     return out
 
 
@@ -948,24 +977,25 @@ def _gradient_table(grads, out):
     grads = list(grads)
     _need(len(grads) > 0, "no gradients")
     _need(out is None or len(out) == len(grads), "out must have one tensor for each gradient")
-    bf16, f32, dev = torch.bfloat16, torch.float32, torch.cuda.current_device()
+    bf16, f32, dev = torch.bfloat16, torch.float32, _device()
     flat = array.array("q")
     for i, g in enumerate(grads):
         dt = g.dtype
-        _need((dt is bf16 or dt is f32) and g.is_cuda and g.get_device() == dev and
-              g.is_contiguous(),
-              "gradients must be contiguous bfloat16 or float32 tensors on the current CUDA device")
+        if not ((dt is bf16 or dt is f32) and g.is_cuda and g.get_device() == dev and
+                g.is_contiguous()):
+            raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on the "
+                             "current CUDA device")
         to = g
         if out is not None:
             to = out[i]
-            _need(to.dtype is dt and to.is_cuda and to.get_device() == dev and
-                  to.is_contiguous() and to.shape == g.shape,
-                  "out must have the gradients' shapes, types and device, and be contiguous")
+            if not (to.dtype is dt and to.is_cuda and to.get_device() == dev and
+                    to.is_contiguous() and to.shape == g.shape):
+                raise ValueError("out must have the gradients' shapes, types and device, and be "
+                                 "contiguous")
         flat.extend((g.data_ptr(), to.data_ptr(), g.numel(), FP32 if dt is f32 else BF16))
     lib = load()
-    ws = torch.empty((lib.latentmoe_grad_workspace(len(grads)),), dtype=torch.uint8,
-                     device=grads[0].device)
-    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+    ws = grads[0].new_empty(lib.latentmoe_grad_workspace(len(grads)), dtype=torch.uint8)
+    norm = grads[0].new_empty(1, dtype=f32)
     return flat, len(grads), norm, ws
 
 

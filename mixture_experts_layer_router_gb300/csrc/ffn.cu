@@ -29,6 +29,8 @@ struct latentmoe_ffn {
   __nv_bfloat16* h = nullptr;   // [max_tokens, F]
   __nv_bfloat16* dg = nullptr;  // training only
   __nv_bfloat16* du = nullptr;
+  __nv_bfloat16* xs = nullptr;  // [8, d]: x and dy of fewer tokens than that
+  __nv_bfloat16* dys = nullptr;
   unsigned* status = nullptr;
   float* parts = nullptr;   // of the kernel for few tokens
   int* arrived = nullptr;
@@ -138,21 +140,52 @@ double plan(FfnArgs& a, int epi, int shape, int sms) {
   return even > longest ? even : longest;
 }
 
+// ns a k-block, measured for the Newton-Schulz products, whose main loop is the same:
+// single tiles are bound by the 64 bytes a clock that an SM takes in.
+constexpr double kSingleBlock = 320.0, kPairBlock = 310.0;
+
 int run(latentmoe_ffn* h, Launch& l, int epi, cudaStream_t s) {
   if (!l.ok) return LATENTMOE_ERR_CUDA;
   const lmoe::PdlScope pdl(true);
-  // ns a k-block, measured for the Newton-Schulz products, whose main loop is the same:
-  // single tiles are bound by the 64 bytes a clock that an SM takes in
   int shape = h->mode;
   if (shape > lmoe::kFfnPair) {
-    const double single = 320.0 * plan(l.a, epi, lmoe::kFfnSingle, h->sms);
-    const double pair = 310.0 * plan(l.a, epi, lmoe::kFfnPair, h->sms);
+    const double single = kSingleBlock * plan(l.a, epi, lmoe::kFfnSingle, h->sms);
+    const double pair = kPairBlock * plan(l.a, epi, lmoe::kFfnPair, h->sms);
     shape = pair <= single ? lmoe::kFfnPair : lmoe::kFfnSingle;
   }
   plan(l.a, epi, shape, h->sms);
   FFN_CK(h, lmoe::launch_ffn(epi, shape, l.a, h->sms, s));
   h->launches += 1;
   return LATENTMOE_OK;
+}
+
+// The time of a launch of one product in ns, on whichever tiles take less: whole rounds
+// of tiles, each its k-blocks.
+double tile_time(long long M, long long N, long long K, int epi, int sms) {
+  FfnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.products = 1;
+  a.p[0].M = static_cast<int>(M);
+  a.p[0].N = static_cast<int>(N);
+  a.p[0].k_blocks = static_cast<int>(ceil_div(K, lmoe::kFfnBK));
+  a.p[0].segments = 1;
+  const double single = kSingleBlock * plan(a, epi, lmoe::kFfnSingle, sms);
+  const double pair = kPairBlock * plan(a, epi, lmoe::kFfnPair, sms);
+  return single < pair ? single : pair;
+}
+
+// Whether the forward of T tokens takes the kernel for few: the weights at 6.2 TB/s, and
+// 0.22 us a token for the parts' way through memory, against whole rounds of tiles. In us,
+// few / tiles: 8704 x 10240 1 token 89 / 451, 27 tokens 97 / 152, 128 tokens 128 / 154;
+// 4096 x 2048 16 tokens 20 / 39, 64 tokens 34 / 36, 96 tokens 44 / 36; 2048 x 2048 48 tokens
+// 23 / 26, 96 tokens 34 / 26.
+bool few_wins(const latentmoe_ffn* h, long long T) {
+  if (T > lmoe::kFewMost) return false;
+  if (T < lmoe::kFfnLeastRows) return true;  // tiles are slow with operands of few rows
+  const double few = 6.0 * h->d * h->F / 6200.0 + 1000.0 + 220.0 * T;
+  const double tiles = tile_time(T, h->F, h->d, lmoe::kFfnGateUp, h->sms) +
+                       tile_time(T, h->d, h->F, lmoe::kFfnPlain, h->sms);
+  return few < tiles;
 }
 
 // One product for few tokens: out [T, rows] of x [T, K] and weights [rows, K].
@@ -213,7 +246,9 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
     delete h;
     return LATENTMOE_ERR_CUDA;
   }
-  const size_t rows = (static_cast<size_t>(p.max_tokens) * p.ffn * 2 + 1023) / 1024 * 1024;
+  const long long most = p.max_tokens < lmoe::kFfnLeastRows ? lmoe::kFfnLeastRows : p.max_tokens;
+  const size_t rows = (static_cast<size_t>(most) * p.ffn * 2 + 1023) / 1024 * 1024;
+  const size_t pad = (static_cast<size_t>(lmoe::kFfnLeastRows) * p.hidden * 2 + 1023) / 1024 * 1024;
   const long long few = p.max_tokens < lmoe::kFewMost ? p.max_tokens : lmoe::kFewMost;
   const size_t parts = static_cast<size_t>(h->sms) * 2 * 128 * 4 *
                        static_cast<size_t>(lmoe::few_tokens(static_cast<int>(few)));
@@ -222,7 +257,7 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
   // status word and arrival counts, parts, h (dg, du)
   h->arrived_bytes = static_cast<size_t>(tiles) * 4;
   const size_t head = (1024 + h->arrived_bytes + 1023) / 1024 * 1024;
-  const size_t bytes = head + parts + rows * (h->training ? 3 : 1);
+  const size_t bytes = head + parts + (h->training ? 3 * rows + 2 * pad : rows);
   e = cudaMalloc(&h->ws, bytes);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -238,6 +273,8 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
   if (h->training) {
     h->dg = reinterpret_cast<__nv_bfloat16*>(base + rows);
     h->du = reinterpret_cast<__nv_bfloat16*>(base + 2 * rows);
+    h->xs = reinterpret_cast<__nv_bfloat16*>(base + 3 * rows);
+    h->dys = reinterpret_cast<__nv_bfloat16*>(base + 3 * rows + pad);
   }
   e = cudaMemset(h->status, 0, head);
   if (e != cudaSuccess) {
@@ -271,7 +308,7 @@ int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, con
   FFN_CK(h, cudaSetDevice(h->device));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
   const long long d = h->d, F = h->F;
-  if (T <= lmoe::kFewMost && h->mode >= 2) {
+  if (h->mode == 3 ? T <= lmoe::kFewMost : h->mode == 2 && few_wins(h, T)) {
     const int rc = run_few(h, lmoe::kFfnGateUp, {x, T, d, ld_x}, w->w_g, w->w_u, F, false, h->h, F,
                            gate, up, s);
     if (rc != LATENTMOE_OK) return rc;
@@ -317,12 +354,25 @@ int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
   FFN_CK(h, cudaSetDevice(h->device));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
   const long long d = h->d, F = h->F;
-  const Mat dy = {g.dy, T, d, g.ld_dy}, x = {g.x, T, d, g.ld_x};
-  const Mat hm = {h->h, T, F, F}, dg = {h->dg, T, F, F}, du = {h->du, T, F, F};
+  // rows of the operands: those past T are zeros
+  const long long R = T < lmoe::kFfnLeastRows ? lmoe::kFfnLeastRows : T;
+  Mat dy = {g.dy, T, d, g.ld_dy}, x = {g.x, T, d, g.ld_x};
+  if (R > T) {
+    const lmoe::PdlScope pdl(true);
+    FFN_CK(h, lmoe::launch_ffn_pad(static_cast<const __nv_bfloat16*>(g.x), g.ld_x,
+                                   static_cast<const __nv_bfloat16*>(g.dy), g.ld_dy,
+                                   static_cast<int>(T), static_cast<int>(d), static_cast<int>(F),
+                                   h->xs, h->dys, h->h, h->dg, h->du, s));
+    h->launches += 1;
+    dy = {h->dys, R, d, d};
+    x = {h->xs, R, d, d};
+  }
+  const Mat hm = {h->h, R, F, F}, dg = {h->dg, R, F, F}, du = {h->du, R, F, F};
   Launch l(h);
   FfnProduct& p = l.add(dy, false, {w->w_d, d, F, F}, true, T, F, d);
   l.ok = l.ok && chunk(&l.a.gate, {g.gate, T, F, F}) && chunk(&l.a.up, {g.up, T, F, F}) &&
-         chunk(&p.out[0], dg) && chunk(&p.out[1], du) && chunk(&p.out[2], hm);
+         chunk(&p.out[0], {h->dg, T, F, F}) && chunk(&p.out[1], {h->du, T, F, F}) &&
+         chunk(&p.out[2], {h->h, T, F, F});
   const int rc = run(h, l, lmoe::kFfnDGate, s);
   if (rc != LATENTMOE_OK) return rc;
   Launch m(h);

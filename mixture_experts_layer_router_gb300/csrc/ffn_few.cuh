@@ -11,9 +11,9 @@
 // parts in the order of the CTAs, so results do not depend on who that is, and
 // finishes it: activation and product, or the rounding to bf16.
 //
-// The second product's launch brings in its first weights while the first product
-// still runs (programmatic dependent launch; two CTAs fit an SM), and waits for it
-// only before it reads h.
+// The second product's CTAs bring in their first weights where the first product's
+// have left an SM (programmatic dependent launch), and wait for the whole of it only
+// before they read h.
 //
 //   warp 0      TMA producer (one lane)
 //   warp 1      TMEM allocator, MMA issuer (one lane)
@@ -27,15 +27,14 @@ namespace lmoe {
 constexpr int kFewThreads = 64 + 128;
 constexpr int kFewWBytes = 128 * kFfnBK * 2;
 __host__ __device__ constexpr int few_stages(int nt) {
-  return nt == 16 ? 6 : nt == 32 ? 5 : nt == 64 ? 4 : 3;
+  return nt == 16 ? 11 : nt == 32 ? 10 : nt == 64 ? 8 : 6;
 }
 __host__ __device__ constexpr int few_stage_bytes(int nt) { return kFewWBytes + nt * kFfnBK * 2; }
 __host__ __device__ constexpr int few_smem_bytes(int nt) {
   return 1024 + few_stages(nt) * few_stage_bytes(nt) + 8 * (2 * few_stages(nt) + 2 + 2 + 1) + 32;
 }
-// two CTAs an SM (233,472 bytes, 1 KB of each reserved)
-static_assert(few_smem_bytes(16) <= 115712 && few_smem_bytes(32) <= 115712 &&
-                  few_smem_bytes(64) <= 115712 && few_smem_bytes(128) <= 115712,
+static_assert(few_smem_bytes(16) <= 232448 && few_smem_bytes(32) <= 232448 &&
+                  few_smem_bytes(64) <= 232448 && few_smem_bytes(128) <= 232448,
               "shared memory of the kernel for few tokens");
 
 // First unit (k-block of the sequence) of CTA c of n.
@@ -62,27 +61,42 @@ __device__ __forceinline__ bool few_all(bool ok) {
   return all != 0;
 }
 
-// The sums of a tile's row r for tokens n, n + step, ...: kFewBatch of them at a
-// time on their way.
-constexpr int kFewBatch = 4;
+// The sums of a tile's rows r[0], r[1], ... for tokens n, n + step, ...: kFewBatch
+// tokens of two parts at a time on their way.
+constexpr int kFewBatch = 8;
+template <int ROWS>
 __device__ __forceinline__ void few_sum(const float* parts, long long part, int c0, int c1,
-                                        int tokens, int n, int step, int r, float (&s)[kFewBatch]) {
+                                        int tokens, int n, int step, const int (&r)[ROWS],
+                                        float (&s)[ROWS][kFewBatch]) {
 #pragma unroll
-  for (int j = 0; j < kFewBatch; ++j) s[j] = 0.0f;
-  for (int c = c0; c <= c1; ++c) {
-    // of the CTA that begins the tile its last part, of the others their first
-    const float* from = parts + (2ll * c + (c > c0 ? 0 : 1)) * part + r;
-    float v[kFewBatch];
+  for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-    for (int j = 0; j < kFewBatch; ++j)
-      v[j] = n + j * step < tokens ? __ldcg(from + (n + j * step) * 128) : 0.0f;
+    for (int j = 0; j < kFewBatch; ++j) s[i][j] = 0.0f;
+  for (int c = c0; c <= c1; c += 2) {
+    float v[2][ROWS][kFewBatch];
 #pragma unroll
-    for (int j = 0; j < kFewBatch; ++j) s[j] += v[j];
+    for (int h = 0; h < 2; ++h) {
+      // of the CTA that begins the tile its last part, of the others their first
+      const float* from = parts + (2ll * (c + h) + (c + h > c0 ? 0 : 1)) * part;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < kFewBatch; ++j)
+          v[h][i][j] = c + h <= c1 && n + j * step < tokens
+                           ? __ldcg(from + (n + j * step) * 128 + r[i])
+                           : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < kFewBatch; ++j) s[i][j] += v[h][i][j];
   }
 }
 
 template <int EPI, int NT>
-__global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kStages = few_stages(NT);
   constexpr int kStage = few_stage_bytes(NT);
   constexpr int kTmem = 2 * NT;  // two accumulators; at least 32 columns
@@ -129,10 +143,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
 
-  // brings weights of unit u into a stage
-  auto load_w = [&](long long u, int stage, uint64_t pol) {
-    const int tile = static_cast<int>(u / a.k_blocks);
-    const int k0 = static_cast<int>(u - static_cast<long long>(tile) * a.k_blocks) * kFfnBK;
+  const int n_units = static_cast<int>(u1 - u0);
+  // brings weights of a tile's k-block into a stage
+  auto load_w = [&](int tile, int kb, int stage, uint64_t pol) {
+    const int k0 = kb * kFfnBK;
     uint8_t* dst = ring + stage * kStage;
     if (EPI == kFfnGateUp) {
       tma_load_2d(&a.w[0], &full_bar[stage], dst, k0, tile * 64, pol);
@@ -150,23 +164,31 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
       if (EPI == kFfnGateUp) tma_prefetch_desc(&a.w[1]);
       tma_prefetch_desc(&a.x);
       const uint64_t pol = policy_evict_first(), pol_x = policy_evict_last();
-      const int early =
-          a.early ? static_cast<int>(u1 - u0 < kStages ? u1 - u0 : kStages) : 0;
-      for (int i = 0; i < early; ++i) {
-        mbar_arrive_expect_tx(&full_bar[i], kStage);
-        load_w(u0 + i, i, pol);
-      }
+      // the units in turn: a division for each would take as long as its copies
+      int tile = static_cast<int>(u0 / a.k_blocks);
+      int kb = static_cast<int>(u0 - static_cast<long long>(tile) * a.k_blocks);
+      int x_kb = kb;
+      const int early = a.early ? (n_units < kStages ? n_units : kStages) : 0;
+      auto next_w = [&](int stage) {
+        mbar_arrive_expect_tx(&full_bar[stage], kStage);
+        load_w(tile, kb, stage, pol);
+        if (++kb == a.k_blocks) {
+          kb = 0;
+          ++tile;
+        }
+      };
+      for (int i = 0; i < early; ++i) next_w(i);
       pdl_wait();
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
-      for (long long u = u0; u < u1; ++u) {
-        if (u - u0 >= early) {
+      for (int i = 0; i < n_units; ++i) {
+        if (i >= early) {
           if (!wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag, a.status)) break;
-          mbar_arrive_expect_tx(&full_bar[stage], kStage);
-          load_w(u, stage, pol);
+          next_w(stage);
         }
-        tma_load_2d(&a.x, &full_bar[stage], ring + stage * kStage + kFewWBytes,
-                    static_cast<int>(u % a.k_blocks) * kFfnBK, 0, pol_x);
+        tma_load_2d(&a.x, &full_bar[stage], ring + stage * kStage + kFewWBytes, x_kb * kFfnBK, 0,
+                    pol_x);
+        if (++x_kb == a.k_blocks) x_kb = 0;
         issued_mask |= 1u << stage;
         issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == kStages) {
@@ -273,17 +295,17 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
           const int r = e & 63, f = tile * 64 + r;
           if (f < a.rows) {
             for (int n = e >> 6; n < a.tokens; n += 2 * kFewBatch) {
-              float g[kFewBatch], v[kFewBatch];
-              few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 2, r, g);
-              few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 2, 64 + r, v);
+              const int both[2] = {r, 64 + r};
+              float s[2][kFewBatch];
+              few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 2, both, s);
 #pragma unroll
               for (int j = 0; j < kFewBatch; ++j) {
                 const long long t = n + 2 * j;
                 if (t >= a.tokens) break;
-                a.out[t * a.ld + f] = __float2bfloat16_rn(g[j] * ffn_sigmoid(g[j]) * v[j]);
+                a.out[t * a.ld + f] = __float2bfloat16_rn(s[0][j] * ffn_sigmoid(s[0][j]) * s[1][j]);
                 if (a.gate != nullptr) {
-                  a.gate[t * a.rows + f] = __float2bfloat16_rn(g[j]);
-                  a.up[t * a.rows + f] = __float2bfloat16_rn(v[j]);
+                  a.gate[t * a.rows + f] = __float2bfloat16_rn(s[0][j]);
+                  a.up[t * a.rows + f] = __float2bfloat16_rn(s[1][j]);
                 }
               }
             }
@@ -292,11 +314,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
           const int f = tile * 128 + e;
           if (f < a.rows) {
             for (int n = 0; n < a.tokens; n += kFewBatch) {
-              float v[kFewBatch];
-              few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 1, e, v);
+              const int one[1] = {e};
+              float s[1][kFewBatch];
+              few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 1, one, s);
 #pragma unroll
               for (int j = 0; j < kFewBatch; ++j)
-                if (n + j < a.tokens) a.out[(n + j) * a.ld + f] = __float2bfloat16_rn(v[j]);
+                if (n + j < a.tokens) a.out[(n + j) * a.ld + f] = __float2bfloat16_rn(s[0][j]);
             }
           }
         }

@@ -44,6 +44,40 @@ static cudaError_t launch_ffn_impl(const FfnArgs& a, int sms, cudaStream_t s) {
                        ffn_smem_bytes(EPI), s, PAIR ? 2 : 1, false, a);
 }
 
+// A CTA a row, 8 channels a thread at a time.
+__global__ void __launch_bounds__(256)
+    ffn_pad_kernel(const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* dy, long long ld_dy,
+                   int tokens, int d, int F, __nv_bfloat16* xs, __nv_bfloat16* dys,
+                   __nv_bfloat16* h, __nv_bfloat16* dg, __nv_bfloat16* du) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row = blockIdx.x;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
+    const long long to = static_cast<long long>(row) * d + c;
+    *reinterpret_cast<uint4*>(dys + to) =
+        row < tokens ? *reinterpret_cast<const uint4*>(dy + row * ld_dy + c) : zero;
+    if (x != nullptr)
+      *reinterpret_cast<uint4*>(xs + to) =
+          row < tokens ? *reinterpret_cast<const uint4*>(x + row * ld_x + c) : zero;
+  }
+  if (row < tokens) return;
+  for (int c = threadIdx.x * 8; c < F; c += 256 * 8) {
+    const long long to = static_cast<long long>(row) * F + c;
+    *reinterpret_cast<uint4*>(h + to) = zero;
+    *reinterpret_cast<uint4*>(dg + to) = zero;
+    *reinterpret_cast<uint4*>(du + to) = zero;
+  }
+}
+
+cudaError_t launch_ffn_pad(const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* dy,
+                           long long ld_dy, int tokens, int d, int F, __nv_bfloat16* xs,
+                           __nv_bfloat16* dys, __nv_bfloat16* h, __nv_bfloat16* dg,
+                           __nv_bfloat16* du, cudaStream_t s) {
+  return launch_kernel(ffn_pad_kernel, dim3(kFfnLeastRows), dim3(256), 0, s, 1, false, x, ld_x, dy,
+                       ld_dy, tokens, d, F, xs, dys, h, dg, du);
+}
+
 cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream_t s) {
   if (epi == kFfnGateUp)
     return shape == kFfnPair ? launch_ffn_impl<kFfnGateUp, kFfnPair>(a, sms, s)

@@ -8,7 +8,7 @@
 // The tensors' bytes form one sequence of tiles that CTAs take in turn, so a large
 // tensor spreads over the GPU and small ones share it.
 //
-// A thread's squares are added in fp32, 32 at a time, and from tile to tile with a
+// A thread's squares are added in fp32, 64 at a time, and from tile to tile with a
 // compensated fp32 sum; sums over threads and CTAs are in 64 bits. Squares that
 // fp32 cannot hold (a thread's sum of a tile above 2^96 or below 2^-80) are added
 // in 64 bits throughout, so the norm is right for any finite numbers. The order of
@@ -78,7 +78,7 @@ __device__ __forceinline__ float grad_squares(const uint4& v, bool f32) {
   }
   return s;
 }
-__device__ __noinline__ double grad_squares64(const uint4& v, bool f32) {
+__device__ __noinline__ double grad_squares64(uint4 v, bool f32) {
   double s = 0.0;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   for (int i = 0; i < 4; ++i) {
@@ -94,14 +94,19 @@ __device__ __noinline__ double grad_squares64(const uint4& v, bool f32) {
   return s;
 }
 
+// The CTA's sum, right in thread 0 alone: 64-bit additions are slow here (a few a
+// clock an SM), so no thread makes one that it does not need.
 __device__ __forceinline__ double block_sum64(double v, double* spare) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_down_sync(0xffffffffu, v, off);
   if ((threadIdx.x & 31) == 0) spare[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kGradThreads / 32 ? spare[threadIdx.x] : 0.0;
 #pragma unroll
-  for (int i = 0; i < kGradThreads / 32; ++i) v += spare[i];
+    for (int off = kGradThreads / 64; off > 0; off >>= 1)
+      v += __shfl_down_sync(0xffffffffu, v, off);
+  }
   return v;
 }
 
@@ -143,11 +148,12 @@ __global__ void __launch_bounds__(kGradThreads)
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The norm from the partial sums, the same in every thread of every CTA.
+// The norm from the partial sums, in thread 0.
 __device__ __forceinline__ double grad_norm_of(const double* partial, int partials, double* spare) {
   double v = 0.0;
   for (int i = threadIdx.x; i < partials; i += kGradThreads) v += partial[i];
-  return sqrt(block_sum64(v, spare));
+  v = block_sum64(v, spare);
+  return threadIdx.x == 0 ? sqrt(v) : 0.0;
 }
 
 __global__ void __launch_bounds__(kGradThreads)
@@ -176,10 +182,15 @@ __global__ void __launch_bounds__(kGradThreads)
   __shared__ double spare[kGradThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
+  __shared__ float factor;
   const double n = grad_norm_of(partial, partials, spare);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = static_cast<float>(n);
-  const double ratio = max_norm / (n + eps);
-  const float c = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);  // NaN stays NaN
+  if (threadIdx.x == 0) {
+    if (norm != nullptr && blockIdx.x == 0) norm[0] = static_cast<float>(n);
+    const double ratio = max_norm / (n + eps);
+    factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);  // NaN stays NaN
+  }
+  __syncthreads();
+  const float c = factor;
   // from the last tile back: what the norm's pass read last is still in L2
   for (unsigned i = blockIdx.x; i < t.tiles; i += gridDim.x) {
     const GradPart p = grad_part(t, t.tiles - 1 - i);
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(kGradThreads)
 }
 
 int grad_ctas(unsigned tiles, int sms) {
-  const unsigned most = 3u * static_cast<unsigned>(sms);
+  const unsigned most = 2u * static_cast<unsigned>(sms);
   return static_cast<int>(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 

@@ -8,7 +8,7 @@ namespace lmoe {
 
 // A tile: what a CTA takes at a time, in 16-byte pieces; kGradPieces a thread.
 constexpr int kGradThreads = 512;
-constexpr int kGradPieces = 4;
+constexpr int kGradPieces = 8;
 constexpr int kGradTile = kGradPieces * kGradThreads;
 
 struct GradEntry {

@@ -6,7 +6,7 @@
 // One pass over dy, s and d_sum: row groups (rows.cuh) take rows t, t + groups,
 // ...; a row sits in registers between its one reduction and dx, and each thread
 // adds up dw for its own channels over all of its group's rows. A second launch
-// adds the groups' partial sums in the order of the groups: results are bitwise
+// adds the CTAs' partial sums in the order of the CTAs: results are bitwise
 // reproducible. Bound by DRAM.
 #include "kernels.h"
 #include "norm.h"
@@ -14,9 +14,17 @@
 
 namespace lmoe {
 
+// Rows that a group takes at a time: all of their accesses are started before the first
+// is used and their sums share a barrier. Two of a bf16 stream (16384 x 6656 with one /
+// two / three: 217 / 182 / 203 us, three spill), one of an fp32 stream, whose rows are
+// twice as long (8192 x 6656: 163 / 161, 16384 x 1024: 44 / 48 us).
+constexpr int norm_rows(int s_size, int vpt) { return vpt > 1 ? 1 : s_size == 2 ? 2 : 1; }
+
 template <typename YT, typename ST, bool DS, bool VEC, int VPT>
-__global__ void __launch_bounds__(512) rms_norm_backward_kernel(const NormBackwardArgs a) {
-  __shared__ float spare[2][32];
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rms_norm_backward_kernel(const NormBackwardArgs a) {
+  constexpr int R = norm_rows(sizeof(ST), VPT);
+  __shared__ float spare[2][R][32];
+  __shared__ float join[8][256];  // dw of the warps of a CTA that has a row a warp
   pdl_wait();
   pdl_launch_dependents();
   const long long groups = static_cast<long long>(gridDim.x) * blockDim.y;
@@ -28,73 +36,125 @@ __global__ void __launch_bounds__(512) rms_norm_backward_kernel(const NormBackwa
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[j][k] = 0.0f;
+  // 8 elements of the weight: in L1 after the first row
+  auto weight = [&](int j, float* w) {
+    if (a.weight_f32)
+      row_load<VEC>(static_cast<const float*>(a.weight), j * warps + warp, lane, d, w);
+    else
+      row_load<VEC>(static_cast<const __nv_bfloat16*>(a.weight), j * warps + warp, lane, d, w);
+  };
   int turn = 0;
-  for (long long t = group; t < a.T; t += groups) {
-    const YT* dy_row = static_cast<const YT*>(a.dy) + t * a.ld_dy;
-    const ST* s_row = static_cast<const ST*>(a.s) + t * a.ld_s;
-    float g[VPT][8], n[VPT][8];
+  for (long long t0 = group; t0 < a.T; t0 += R * groups) {
+    // the rows as they lie in memory, half the registers of their fp32 values
+    RowPiece<VEC, YT> dy[R][VPT];
+    RowPiece<VEC, ST> s[R][VPT], ds[R][VPT];
+    float rstd[R];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) row_load<VEC>(dy_row, j * warps + warp, lane, d, g[j]);
+    for (int r = 0; r < R; ++r) {
+      const long long t = t0 + r * groups;
+      const int width = t < a.T ? d : 0;  // a row past the last is zeros
+      rstd[r] = t < a.T ? a.rstd[t] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) row_load<VEC>(s_row, j * warps + warp, lane, d, n[j]);
-    const float rstd = a.rstd[t];
-    float dot = 0.0f;
+      for (int j = 0; j < VPT; ++j) {
+        const int chunk = j * warps + warp;
+        dy[r][j].load(static_cast<const YT*>(a.dy) + t * a.ld_dy, chunk, lane, width);
+        s[r][j].load(static_cast<const ST*>(a.s) + t * a.ld_s, chunk, lane, width);
+        if (DS) ds[r][j].load(static_cast<const ST*>(a.d_sum) + t * a.ld_d_sum, chunk, lane, width);
+      }
+    }
+    float dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) dot[r] = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       float w[8];
-      if (a.weight_f32)
-        row_load<VEC>(static_cast<const float*>(a.weight), j * warps + warp, lane, d, w);
-      else
-        row_load<VEC>(static_cast<const __nv_bfloat16*>(a.weight), j * warps + warp, lane, d, w);
-      float part = 0.0f;
+      weight(j, w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        n[j][k] *= rstd;
-        dw[j][k] = fmaf(g[j][k], n[j][k], dw[j][k]);
-        g[j][k] *= w[k];
-        part = fmaf(g[j][k], n[j][k], part);
+      for (int r = 0; r < R; ++r) {
+        float g[8], n[8];
+        dy[r][j].get(g);
+        s[r][j].get(n);
+        float part = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          n[k] *= rstd[r];
+          dw[j][k] = fmaf(g[k], n[k], dw[j][k]);
+          part = fmaf(g[k] * w[k], n[k], part);
+        }
+        dot[r] += part;
       }
-      dot += part;
     }
-    // two barriers' buffers in turn: a row's sums are read before the next row's
-    // barrier, so the row after that may write them again
-    const float mean = group_sum(dot, spare[turn]) / static_cast<float>(d);
-    turn ^= 1;
-    ST* to = static_cast<ST*>(a.dx) + t * a.ld_dx;
+    // sums over the group; two buffers in turn: an iteration's sums are read before the
+    // next one's barrier, so the one after that may write them again
+#pragma unroll
+    for (int r = 0; r < R; ++r) dot[r] = warp_sum(dot[r]);
+    if (warps > 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) spare[turn][r][warp] = dot[r];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r) dot[r] = warp_sum(lane < warps ? spare[turn][r][lane] : 0.0f);
+      turn ^= 1;
+    }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int chunk = j * warps + warp;
-      float o[8];
-      if constexpr (DS) {
-        row_load<VEC>(static_cast<const ST*>(a.d_sum) + t * a.ld_d_sum, chunk, lane, d, o);
-      } else {
+      float w[8];
+      weight(j, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+      for (int r = 0; r < R; ++r) {
+        const long long t = t0 + r * groups;
+        if (t >= a.T) break;
+        const float back = rstd[r] * (dot[r] / static_cast<float>(d));
+        float g[8], n[8], o[8];
+        dy[r][j].get(g);
+        s[r][j].get(n);
+        if constexpr (DS) {
+          ds[r][j].get(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] += rstd[r] * (g[k] * w[k] - n[k] * back);
+        row_store<VEC>(static_cast<ST*>(a.dx) + t * a.ld_dx, chunk, lane, d, o);
+        if (sizeof(ST) == 4 && a.dx16 != nullptr)
+          row_store<VEC>(static_cast<__nv_bfloat16*>(a.dx16) + t * a.ld_dx16, chunk, lane, d, o);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] += rstd * (g[j][k] - n[j][k] * mean);
-      row_store<VEC>(to, chunk, lane, d, o);
-      if (sizeof(ST) == 4 && a.dx16 != nullptr)
-        row_store<VEC>(static_cast<__nv_bfloat16*>(a.dx16) + t * a.ld_dx16, chunk, lane, d, o);
     }
   }
-  if (a.dw != nullptr) {
-    float* to = a.partial + group * d;
+  if (a.dw == nullptr) return;
+  if (VPT == 1 && blockDim.y > 1) {
+    // one row of partial sums a CTA: its warps' in their order
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      // [groups, d] of the library's own: whole vectors where d allows
-      if (d % 8 == 0)
-        row_store<VEC>(to, j * warps + warp, lane, d, dw[j]);
-      else
-        row_store<false>(to, j * warps + warp, lane, d, dw[j]);
+    for (int k = 0; k < 8; ++k) join[threadIdx.y][(VEC ? 8 * lane + k : 32 * k + lane)] = dw[0][k];
+    __syncthreads();
+    const int c = threadIdx.y * 32 + lane;  // eight warps: 256 channels
+    if (c < d) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += join[i][c];
+      a.partial[static_cast<long long>(blockIdx.x) * d + c] = sum;
     }
+    return;
+  }
+  float* to = a.partial + static_cast<long long>(blockIdx.x) * d;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    // [CTAs, d] of the library's own: whole vectors where d allows
+    if (d % 8 == 0)
+      row_store<VEC>(to, j * warps + warp, lane, d, dw[j]);
+    else
+      row_store<false>(to, j * warps + warp, lane, d, dw[j]);
   }
 }
 
-constexpr int kDwRows = 16;
+constexpr int kDwRows = 32;
 
-// dw[c] = sum over the groups of partial[group][c]: 32 columns a CTA, kDwRows
-// threads a column.
+// dw[c] = sum over the CTAs of partial[CTA][c]: 32 columns a CTA, kDwRows threads
+// a column.
 __global__ void __launch_bounds__(32 * kDwRows)
     rms_norm_dw_kernel(const float* partial, int groups, int d, float* dw) {
   __shared__ float part[kDwRows][33];
@@ -126,14 +186,14 @@ struct Shape {
 Shape shape_of(long long T, int d, int sms) {
   Shape p;
   const int chunks = (d + 255) / 256;
-  p.vpt = chunks <= 4 ? 1 : chunks <= 16 ? 2 : 4;
+  p.vpt = chunks <= 32 ? 1 : 4;
   p.warps = (chunks + p.vpt - 1) / p.vpt;
-  p.rows = p.warps == 1 ? 8 : 1;
-  // about 32 warps an SM
+  p.rows = p.warps == 1 ? 8 : 1;  // eight: what the kernel joins
+  // about 32 warps an SM: 24 / 32 / 40 take 22 / 20 / 22 us for 4096 x 2048 in bf16
   int per_sm = 32 / (p.warps * p.rows);
   if (per_sm < 1) per_sm = 1;
-  const long long want = (T + p.rows - 1) / p.rows;
-  p.ctas = static_cast<int>(want < static_cast<long long>(per_sm) * sms ? want : per_sm * sms);
+  const long long want = (T + p.rows - 1) / p.rows, most = static_cast<long long>(per_sm) * sms;
+  p.ctas = static_cast<int>(want < most ? want : most);
   return p;
 }
 
@@ -143,9 +203,8 @@ bool whole(const void* p, long long ld, int size, int unit) {
 
 template <typename YT, typename ST, bool DS, bool VEC>
 cudaError_t launch_vpt(const NormBackwardArgs& a, const Shape& p, cudaStream_t s) {
-  const auto kern = p.vpt == 1   ? rms_norm_backward_kernel<YT, ST, DS, VEC, 1>
-                    : p.vpt == 2 ? rms_norm_backward_kernel<YT, ST, DS, VEC, 2>
-                                 : rms_norm_backward_kernel<YT, ST, DS, VEC, 4>;
+  const auto kern = p.vpt == 1 ? rms_norm_backward_kernel<YT, ST, DS, VEC, 1>
+                               : rms_norm_backward_kernel<YT, ST, DS, VEC, 4>;
   return launch_kernel(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(32 * p.warps, p.rows), 0, s,
                        1, false, a);
 }
@@ -169,8 +228,7 @@ cudaError_t launch_sum(const NormBackwardArgs& a, const Shape& p, cudaStream_t s
 }  // namespace
 
 int norm_partials(long long T, int d, int sms) {
-  const Shape p = shape_of(T, d, sms);
-  return p.ctas * p.rows;
+  return shape_of(T, d, sms).ctas;
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, int sms, cudaStream_t s) {
@@ -185,7 +243,7 @@ cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, int sms, cudaStr
   if (e != cudaSuccess || a.dw == nullptr) return e;
   return launch_kernel(rms_norm_dw_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)),
                        dim3(32, kDwRows), 0, s, 1, false, static_cast<const float*>(a.partial),
-                       p.ctas * p.rows, a.d, a.dw);
+                       p.ctas, a.d, a.dw);
 }
 
 }  // namespace lmoe

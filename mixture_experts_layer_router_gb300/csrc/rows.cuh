@@ -42,29 +42,49 @@ __device__ __forceinline__ uint4 float_to_bf16x8(const float* x) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// Elements of chunk `chunk` that this lane holds; those at or past d are zero.
+// Elements of chunk `chunk` that this lane holds, as they come from memory; those at
+// or past d are zero. load() only starts the accesses.
 template <bool VEC, typename T>
-__device__ __forceinline__ void row_load(const T* row, int chunk, int lane, int d, float* x) {
-  if constexpr (VEC) {
-    const int e = chunk * 256 + lane * 8;
-    if (e < d) {
-      if constexpr (sizeof(T) == 2) {
-        bf16x8_to_float(*reinterpret_cast<const uint4*>(row + e), x);
-      } else {
-        const float4 a = reinterpret_cast<const float4*>(row + e)[0];
-        const float4 b = reinterpret_cast<const float4*>(row + e)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = 0.0f;
-    }
-  } else {
+struct RowPiece {
+  float x[8];
+  __device__ __forceinline__ void load(const T* row, int chunk, int lane, int d) {
     const int e = chunk * 256 + lane;
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = e + 32 * k < d ? RowType<T>::get(row[e + 32 * k]) : 0.0f;
   }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = x[k];
+  }
+};
+template <>
+struct RowPiece<true, __nv_bfloat16> {
+  uint4 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int chunk, int lane, int d) {
+    const int e = chunk * 256 + lane * 8;
+    x = e < d ? *reinterpret_cast<const uint4*>(row + e) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* v) const { bf16x8_to_float(x, v); }
+};
+template <>
+struct RowPiece<true, float> {
+  float4 x[2];
+  __device__ __forceinline__ void load(const float* row, int chunk, int lane, int d) {
+    const int e = chunk * 256 + lane * 8;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    x[0] = e < d ? reinterpret_cast<const float4*>(row + e)[0] : zero;
+    x[1] = e < d ? reinterpret_cast<const float4*>(row + e)[1] : zero;
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = x[0].x; v[1] = x[0].y; v[2] = x[0].z; v[3] = x[0].w;
+    v[4] = x[1].x; v[5] = x[1].y; v[6] = x[1].z; v[7] = x[1].w;
+  }
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_load(const T* row, int chunk, int lane, int d, float* x) {
+  RowPiece<VEC, T> p;
+  p.load(row, chunk, lane, d);
+  p.get(x);
 }
 
 template <bool VEC, typename T>

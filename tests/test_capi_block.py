@@ -56,7 +56,7 @@ def grad(**kw):
     (dict(dy=None), 4, 64, A, 1 << 30, INVALID), (dict(s=None), 4, 64, A, 1 << 30, INVALID),
     (dict(weight=None), 4, 64, A, 1 << 30, INVALID), (dict(rstd=None), 4, 64, A, 1 << 30, INVALID),
     (dict(dx=None), 4, 64, A, 1 << 30, INVALID), (dict(dx16=A), 4, 64, A, 1 << 30, INVALID),
-    (dict(dw=A), 4, 64, None, 1 << 30, INVALID), (dict(dw=A), 4, 64, A, 4 * 64 * 4 - 1, INVALID),
+    (dict(dw=A), 4, 64, None, 1 << 30, INVALID), (dict(dw=A), 4, 64, A, 64 * 4 - 1, INVALID),
     (dict(s_dtype=9), 4, 64, A, 1 << 30, INVALID), (dict(ld_dx=8), 4, 64, A, 1 << 30, INVALID),
     (dict(), 0, 64, A, 1 << 30, INVALID), (dict(), 4, 20000, A, 1 << 30, UNSUPPORTED),
     (dict(dw=A), 4, 64, A + 8, 1 << 30, UNSUPPORTED), (dict(dy=A + 1), 4, 64, A, 1 << 30, UNSUPPORTED),
@@ -71,7 +71,7 @@ def test_norm_null(lib):
     assert lib.latentmoe_rms_norm_backward(None, 1, 1, None, 0, None) == INVALID
     size = lib.latentmoe_rms_norm_backward_workspace
     assert size(0, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0
-    assert size(4, 1024) >= 4 * 1024 * 4
+    assert size(4, 1024) >= 1024 * 4
     assert size(1 << 20, 1024) <= 256 * 32 * 1024 * 4
 
 

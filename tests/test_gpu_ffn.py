@@ -70,7 +70,8 @@ def check(got, exact, size, K, out=BF16):
 
 # one row, fewer rows and columns than a tile has, borders of the tiles (64, 128, 256)
 # and their neighbours, several tiles in every direction
-SIZES = [(1, 8, 8), (1, 256, 512), (3, 16, 24), (17, 1024, 640), (64, 64, 64), (65, 72, 200), (128, 256, 256),
+# (and 7 and 8 rows: the border of the padded operands)
+SIZES = [(1, 8, 8), (1, 256, 512), (7, 200, 136), (8, 136, 200), (3, 16, 24), (17, 1024, 640), (64, 64, 64), (65, 72, 200), (128, 256, 256),
          (129, 136, 1032), (255, 264, 520), (256, 512, 128), (257, 1032, 136), (777, 1336, 2040),
          (1000, 128, 1024), (2048, 256, 384)]
 

@@ -1,8 +1,9 @@
 """Global gradient norm and clipping against float64.
 
-Tolerances. u = 2^-24. A thread adds at most 32 squares in fp32 (one rounding each
-and 35 additions of positive numbers), then compensated fp32 and 64-bit sums: at most
-38 u of the sum, 19 u of the norm, and its own rounding. NORM = 24 u. The factor is as
+Tolerances. u = 2^-24. A thread adds at most 64 squares of a tile in fp32 (one rounding
+each; eight sums of eight, so no number goes through more than 16 additions), then
+compensated fp32 and 64-bit sums: below 38 u of the sum, 19 u of the norm, and its own
+rounding. NORM = 24 u. The factor is as
 exact, and a product is rounded once: half a step of the type.
 """
 import ctypes

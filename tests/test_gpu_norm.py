@@ -14,8 +14,10 @@ Codes: the nearest E4M3 number of y / scale, off by half a step of E4M3 (a step 
 Gradient. dx = d_sum + rstd (a - n m), m = mean(a n): a, n are off by 2 u of
 themselves, m by at most (8 + 4 + 10 + 4) u of mean |a n|, the last three operations by
 u of what they add: 8 u (|d_sum| + rstd (|a| + |n m|)) + 30 u rstd |n| mean |a n|.
-dw = sum of dy n over the tokens: at most N = rows of a group + groups / 16 + 20
-additions in a row, each off by u of the sum of the magnitudes, and 3 u a term.
+dw = sum of dy n over the tokens: a group's rows one after another (152 groups or more,
+or a row each), the 8 groups of a CTA, then at most 608 CTAs in 32 chains of 19, and the
+32: at most N = rows of a group + 8 + 19 + 32 additions in a row, each off by u of the
+sum of the magnitudes, and 3 u a term.
 """
 import pytest
 import torch
@@ -243,7 +245,7 @@ def test_backward(T, d, yt, st):
             assert torch.equal(got["dx16"], got["dx"].to(BF16))
         rows = 8 if d <= 256 else 1
         groups = max(1, min(-(-T // rows) * rows, 152))
-        n = -(-T // groups) + 10 + 20 + 3
+        n = -(-T // groups) + 8 + 19 + 32 + 3
         assert bool(((got["dw"].double() - dw).abs() <= n * U * size).all())
         again = capi.rms_norm_backward(dy, s, w, rstd, d_sum=ds)
         assert torch.equal(again["dx"], got["dx"]) and torch.equal(again["dw"], got["dw"])
