@@ -35,6 +35,7 @@ struct latentmoe_ffn {
   float* parts = nullptr;   // of the kernel for few tokens
   int* arrived = nullptr;
   size_t arrived_bytes = 0;
+  int* counter = nullptr;   // of the plain products' tiles
   int64_t launches = 0;
   int last_cuda = 0;
 };
@@ -93,6 +94,7 @@ struct Launch {
   explicit Launch(const latentmoe_ffn* h) {
     memset(&a, 0, sizeof(a));
     a.status = h->status;
+    a.counter = h->counter;
   }
   // D [M, N] = A B^T over K: a_mn / b_mn say that the operand lies as [K, M] / [K, N].
   FfnProduct& add(const Mat& A, bool a_mn, const Mat& B, bool b_mn, long long M, long long N,
@@ -113,44 +115,49 @@ struct Launch {
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Tiles for a shape, in the order of the products; the time of the launch in
-// k-blocks of one unit: whole rounds for one product, else the work spread evenly
-// and half of the longest tile for the end.
+// Tiles for a shape, in the order of the products; the expected time of the launch in
+// ns: whole rounds for one product, else the work spread evenly and half of the longest
+// tile for the end. A k-block takes 320 (single) or 310 (pair; measured for the
+// Newton-Schulz products, whose main loop is the same: single tiles are bound by the 64
+// bytes a clock that an SM takes in), a tile at least its epilogue, and the last tile's
+// epilogue is seen in full. us, single / pair: 128 x 256 x 256 forward 9.3 / 12.3, backward 12.9 /
+// 18.5; 1024 x 1024 x 1024 forward 16.4 / 19.5; 300 x 4096 x 4096 dx 64.5 / 76, forward 67 / 55;
+// 777 x 1336 x 2040 forward 42 / 33; 4096 x 2048 x 2048 113 / 77.
 double plan(FfnArgs& a, int epi, int shape, int sms) {
+  const bool pair = shape == lmoe::kFfnPair;
   const int cols = epi == lmoe::kFfnGateUp ? lmoe::ffn_bn(shape) / 2 : lmoe::ffn_bn(shape);
-  const long long units = shape == lmoe::kFfnPair ? sms / 2 : sms;
-  long long tiles = 0, longest = 0;
-  double work = 0.0;
+  const long long units = pair ? sms / 2 : sms;
+  const double block = pair ? 310.0 : 320.0, least = pair ? 2000.0 : 1000.0;
+  const double end = !pair ? 0.0 : epi == lmoe::kFfnDGate ? 4000.0 : 1500.0;
+  long long tiles = 0;
+  double work = 0.0, longest = 0.0;
   for (int i = 0; i < a.products; ++i) {
     FfnProduct& p = a.p[i];
     p.first = static_cast<int>(tiles);
     p.m_tiles = static_cast<int>(ceil_div(p.M, lmoe::ffn_bm(shape)));
     p.n_tiles = static_cast<int>(ceil_div(p.N, cols));
     const long long n = static_cast<long long>(p.m_tiles) * p.n_tiles;
-    const long long kbs = static_cast<long long>(p.k_blocks) * p.segments;
+    double one = block * p.k_blocks * p.segments;
+    if (one < least) one = least;
     tiles += n;
-    work += static_cast<double>(n) * kbs;
-    if (kbs > longest) longest = kbs;
+    work += n * one;
+    if (one > longest) longest = one;
   }
   a.tiles = static_cast<int>(tiles);
-  a.band = shape == lmoe::kFfnPair ? 8 : 16;
+  a.band = pair ? 8 : 16;
   if (units < 1) return 1e30;
-  if (a.products == 1) return static_cast<double>(ceil_div(tiles, units) * longest);
+  if (a.products == 1) return ceil_div(tiles, units) * longest + end;
   const double even = work / units + (tiles > units ? 0.5 * longest : 0.0);
-  return even > longest ? even : longest;
+  return (even > longest ? even : longest) + end;
 }
-
-// ns a k-block, measured for the Newton-Schulz products, whose main loop is the same:
-// single tiles are bound by the 64 bytes a clock that an SM takes in.
-constexpr double kSingleBlock = 320.0, kPairBlock = 310.0;
 
 int run(latentmoe_ffn* h, Launch& l, int epi, cudaStream_t s) {
   if (!l.ok) return LATENTMOE_ERR_CUDA;
   const lmoe::PdlScope pdl(true);
   int shape = h->mode;
   if (shape > lmoe::kFfnPair) {
-    const double single = kSingleBlock * plan(l.a, epi, lmoe::kFfnSingle, h->sms);
-    const double pair = kPairBlock * plan(l.a, epi, lmoe::kFfnPair, h->sms);
+    const double single = plan(l.a, epi, lmoe::kFfnSingle, h->sms);
+    const double pair = plan(l.a, epi, lmoe::kFfnPair, h->sms);
     shape = pair <= single ? lmoe::kFfnPair : lmoe::kFfnSingle;
   }
   plan(l.a, epi, shape, h->sms);
@@ -169,20 +176,20 @@ double tile_time(long long M, long long N, long long K, int epi, int sms) {
   a.p[0].N = static_cast<int>(N);
   a.p[0].k_blocks = static_cast<int>(ceil_div(K, lmoe::kFfnBK));
   a.p[0].segments = 1;
-  const double single = kSingleBlock * plan(a, epi, lmoe::kFfnSingle, sms);
-  const double pair = kPairBlock * plan(a, epi, lmoe::kFfnPair, sms);
+  const double single = plan(a, epi, lmoe::kFfnSingle, sms);
+  const double pair = plan(a, epi, lmoe::kFfnPair, sms);
   return single < pair ? single : pair;
 }
 
 // Whether the forward of T tokens takes the kernel for few: the weights at 6.2 TB/s, and
-// 0.22 us a token for the parts' way through memory, against whole rounds of tiles. In us,
+// 0.25 us a token for the parts' way through memory, against whole rounds of tiles. In us,
 // few / tiles: 8704 x 10240 1 token 89 / 451, 27 tokens 97 / 152, 128 tokens 128 / 154;
 // 4096 x 2048 16 tokens 20 / 39, 64 tokens 34 / 36, 96 tokens 44 / 36; 2048 x 2048 48 tokens
 // 23 / 26, 96 tokens 34 / 26.
 bool few_wins(const latentmoe_ffn* h, long long T) {
   if (T > lmoe::kFewMost) return false;
   if (T < lmoe::kFfnLeastRows) return true;  // tiles are slow with operands of few rows
-  const double few = 6.0 * h->d * h->F / 6200.0 + 1000.0 + 220.0 * T;
+  const double few = 6.0 * h->d * h->F / 6200.0 + 250.0 * T;
   const double tiles = tile_time(T, h->F, h->d, lmoe::kFfnGateUp, h->sms) +
                        tile_time(T, h->d, h->F, lmoe::kFfnPlain, h->sms);
   return few < tiles;
@@ -266,6 +273,7 @@ int latentmoe_ffn_create(const latentmoe_ffn_dims* dims, latentmoe_ffn_t* out) {
   }
   char* base = static_cast<char*>(h->ws);
   h->status = reinterpret_cast<unsigned*>(base);
+  h->counter = reinterpret_cast<int*>(base + 512);
   h->arrived = reinterpret_cast<int*>(base + 1024);
   h->parts = reinterpret_cast<float*>(base + head);
   base += head + parts;
@@ -416,8 +424,11 @@ int latentmoe_ffn_get_status(latentmoe_ffn_t h, uint32_t* device_status) {
   unsigned v = 0;
   FFN_CK(h, cudaMemcpy(&v, h->status, 4, cudaMemcpyDeviceToHost));
   FFN_CK(h, cudaMemset(h->status, 0, 4));
-  // a launch that gave up may have left arrivals
-  if (v != 0) FFN_CK(h, cudaMemset(h->arrived, 0, h->arrived_bytes));
+  // a launch that gave up may have left arrivals and tiles taken
+  if (v != 0) {
+    FFN_CK(h, cudaMemset(h->arrived, 0, h->arrived_bytes));
+    FFN_CK(h, cudaMemset(h->counter, 0, 8));
+  }
   *device_status = v;
   if (v & LATENTMOE_STATUS_TIMEOUT) return LATENTMOE_ERR_TIMEOUT;
   return v != 0 ? LATENTMOE_ERR_DEVICE_STATUS : LATENTMOE_OK;

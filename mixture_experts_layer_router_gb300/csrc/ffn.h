@@ -43,6 +43,7 @@ struct FfnArgs {
   int products;
   int tiles;
   int band;  // m-tiles of a band of the raster
+  int* counter;  // plain: {next tile, units that have ended}, zero; left zero
   unsigned* status;
 };
 cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream_t s);

@@ -23,15 +23,31 @@
 // operands of the next product: 2^-9 of an entry in the mean, as much as the
 // rounding of a bf16 result; keeping them wider would double those products.
 //
+// Order. Tiles of one product are alike and go to the units in turn. Those of the
+// gradient's last launch differ in length (dx: 2 F / 64 k-blocks, dW: tokens / 64), so
+// running units take them from a counter, the longest first (each unit's first tile is its
+// own), towards the end of the one before. us, in turn / from the counter: 777 x 1336 x 2040
+// 66 / 51, 300 x 4096 x 4096 105 / 78, 200 x 8704 x 10240 311 / 251, 512 x 2048 x 2048 51 / 40.
+//
+// What bounds it. An SM takes in 64 bytes a clock: 512 clocks for a k-block's 32 KB, as
+// many as the MMAs of a pair's k-block take (a single tile's take half of them). The
+// producing threads need most of that time too, so each operand has a thread, and nothing
+// else is done in their loops (one thread for both: 2 % slower; taking the tiles in its loop:
+// 14 %; 16 KB boxes chosen at run time: 10 %). Large products run at the clock that the power
+// cap leaves: 8192 x 8704 x 10240 forward 2.8 ms, 1.58 PFLOP/s; 4096 x 2048 x 2048 at the full
+// clock 76 us, 1.36 PFLOP/s, with 3.4 and 1.7 rounds of tiles.
+//
 // Sizes that no tile divides: TMA fills what lies outside an operand with zeros
 // and stores only what lies inside a result; boxes that begin past a result's end
 // are not stored at all.
 //
-//   warp 0      TMA producer (one lane)
+//   warp 0      TMA producer of A (one lane)
 //   warp 1      TMEM allocator, MMA issuer (one lane; pair: the leader's)
+//   warp 11     TMA producer of B (one lane)
 //   warps 2..9  epilogue (TMEM lane quarter warp % 4, alternate 32-column chunks):
 //               a 32 x 32 chunk goes through the warp's slots in shared memory and
 //               leaves (dgate: gate and up also arrive) by TMA
+//   warp 10     takes the tiles from the counter and publishes them (one lane)
 // Tiles: 256 x 256 on SM pairs (cta_group::2), 128 x 128 on one SM; two
 // accumulators in TMEM, one filled while the other is drained.
 #pragma once
@@ -44,9 +60,10 @@ namespace lmoe {
 constexpr int kFfnTileBytes = 128 * kFfnBK * 2;  // 128 rows of one operand
 constexpr int kFfnStageBytes = 2 * kFfnTileBytes;
 constexpr int kFfnEpiWarps = 8;
-constexpr int kFfnThreads = 64 + 32 * kFfnEpiWarps;
+constexpr int kFfnThreads = 128 + 32 * kFfnEpiWarps;
 constexpr int kFfnChunk = 32 * 64;  // 32 x 32 bf16, 64-byte swizzle; fp32: two, 128-byte swizzle
 constexpr int kFfnSlots = 2;
+constexpr int kFfnRing = 2;  // published tiles
 __host__ __device__ constexpr int ffn_stages(int epi) { return epi == kFfnPlain ? 5 : 4; }
 __host__ __device__ constexpr int ffn_slot_bytes(int epi) {
   return epi == kFfnPlain ? 2 * kFfnChunk : 3 * kFfnChunk;
@@ -55,7 +72,8 @@ __host__ __device__ constexpr int ffn_slot_bytes(int epi) {
 // boundaries: 2 KB chunks, whose swizzle patterns repeat every 512 or 1024), barriers.
 __host__ __device__ constexpr int ffn_smem_bytes(int epi) {
   return 1024 + ffn_stages(epi) * kFfnStageBytes + kFfnEpiWarps * kFfnSlots * ffn_slot_bytes(epi) +
-         8 * (2 * ffn_stages(epi) + 2 + 2 + 1 + kFfnEpiWarps * kFfnSlots) + 16;
+         8 * (2 * ffn_stages(epi) + 2 + 2 + 1 + kFfnEpiWarps * kFfnSlots + 2 * kFfnRing + 1) +
+         4 * kFfnRing + 16;
 }
 static_assert(ffn_smem_bytes(kFfnGateUp) <= 232448 && ffn_smem_bytes(kFfnPlain) <= 232448,
               "gated block shared memory");
@@ -133,12 +151,11 @@ __device__ __forceinline__ FfnTile ffn_decode(int t, const FfnArgs& a) {
   return c;
 }
 
-// One operand box: 64 rows or columns mn0.., 64 of K from k0 on.
+// One operand box of 64 x 64 at column c0 and row c1 of the matrix.
 template <bool PAIR>
-__device__ __forceinline__ void ffn_load(const CUtensorMap* map, bool mn, uint64_t* bar,
-                                         uint32_t bar_cluster, uint8_t* dst, int mn0, int k0,
+__device__ __forceinline__ void ffn_load(const CUtensorMap* map, uint64_t* bar,
+                                         uint32_t bar_cluster, uint8_t* dst, int c0, int c1,
                                          uint64_t pol) {
-  const int c0 = mn ? mn0 : k0, c1 = mn ? k0 : mn0;
   if constexpr (PAIR) tma_load_2d_pair(map, bar_cluster, dst, c0, c1, pol);
   else tma_load_2d(map, bar, dst, c0, c1, pol);
 }
@@ -175,6 +192,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   constexpr int kStages = ffn_stages(EPI);
   constexpr int kSlotBytes = ffn_slot_bytes(EPI);
   constexpr int kBN = ffn_bn(SHAPE);
+  // tiles from the counter; of one product they are all alike
+  const bool take = EPI == kFfnPlain && a.products > 1;
+  // readers of a published tile: producers, the MMA issuer, epilogue warps
+  constexpr int kReaders = PAIR ? 5 + 2 * kFfnEpiWarps : 3 + kFfnEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -187,7 +208,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   uint64_t* tempty_bar = tfull_bar + 2;
   uint64_t* done_bar = tempty_bar + 2;
   uint64_t* slot_bar = done_bar + 1;  // [kFfnEpiWarps][kFfnSlots]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(slot_bar + kFfnEpiWarps * kFfnSlots);
+  uint64_t* tr_full = slot_bar + kFfnEpiWarps * kFfnSlots;  // [kFfnRing]
+  uint64_t* tr_empty = tr_full + kFfnRing;                  // [kFfnRing], pair: the leader's is used
+  uint64_t* want_bar = tr_empty + kFfnRing;  // the producer nears its tile's end
+  int* tile_ring = reinterpret_cast<int*>(want_bar + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_ring + kFfnRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -223,6 +248,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     }
     mbar_init(done_bar, 1);
     for (int i = 0; i < kFfnEpiWarps * kFfnSlots; ++i) mbar_init(&slot_bar[i], 1);
+    for (int i = 0; i < kFfnRing; ++i) {
+      mbar_init(&tr_full[i], 1);
+      mbar_init(&tr_empty[i], kReaders);
+    }
+    mbar_init(want_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -250,53 +280,75 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   if constexpr (PAIR) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tr_empty_leader =
+      PAIR ? mapa_shared(smem_addr(&tr_empty[0]), 0) : smem_addr(&tr_empty[0]);
 
-  if (warp == 0) {
+  // The tile after t, for one thread; -1: no more. The arrival needs no release: it
+  // announces a read, made by the time its value is compared.
+  int ring_slot = 0;
+  uint32_t ring_ph = 0;
+  auto next_tile = [&](int t) -> int {
+    if (!take) return t + units < a.tiles ? t + units : -1;
+    if (!wait1(&tr_full[ring_slot], ring_ph)) return -1;
+    t = *reinterpret_cast<volatile int*>(&tile_ring[ring_slot]);
+    if (t >= -1) ffn_arrive_relaxed(tr_empty_leader + 8u * static_cast<uint32_t>(ring_slot));
+    if (++ring_slot == kFfnRing) {
+      ring_slot = 0;
+      ring_ph ^= 1u;
+    }
+    return t;
+  };
+
+  if (warp == 0 || warp == kFfnEpiWarps + 3) {
     if (lane == 0) {
-      // ------------------------------------------------ TMA producer
+      // ------------------------------------------------ TMA producers: A and B
+      const bool of_b = warp != 0;
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      for (int t = unit; t < a.tiles && ok; t += units) {
+      for (int t = unit; ok && t >= 0; t = ok ? next_tile(t) : -1) {
         const FfnTile c = ffn_decode<EPI, SHAPE>(t, a);
         const FfnProduct& p = a.p[c.p];
-        const bool amn = p.a_mn != 0, bmn = p.b_mn != 0;
-        const int arow = c.row0 + rank * 128;
+        const bool mn = (of_b ? p.b_mn : p.a_mn) != 0;
+        // first row or column of the tile's two boxes. gate+up: pair, the gate rows in CTA 0
+        // and the up rows in CTA 1; single, 64 gate rows, then the up rows of the same features
+        const bool both = EPI == kFfnGateUp && of_b;
+        const int row = !of_b ? c.row0 + rank * 128 : both ? c.col0 : c.col0 + rank * 128;
+        const int step = both && !PAIR ? 0 : 64;
+        const int k_blocks = p.k_blocks;
         for (int g = 0; g < p.segments && ok; ++g) {
-          // rows of B in this CTA's two boxes
-          const CUtensorMap *mb0 = &p.b[g], *mb1 = &p.b[g];
-          int brow0, brow1;
-          if (EPI == kFfnGateUp) {
-            if (PAIR) {  // the gate rows in CTA 0, the up rows in CTA 1
-              mb0 = mb1 = &p.b[rank];
-              brow0 = c.col0;
-              brow1 = c.col0 + 64;
-            } else {  // 64 gate rows, then the up rows of the same features
-              mb0 = &p.b[0];
-              mb1 = &p.b[1];
-              brow0 = brow1 = c.col0;
+          const CUtensorMap* m0 = both ? &p.b[PAIR ? rank : 0] : of_b ? &p.b[g] : &p.a[g];
+          const CUtensorMap* m1 = both && !PAIR ? &p.b[1] : m0;
+          // coordinates of the boxes, and what a k-block adds to them
+          int x = mn ? row : 0, y = mn ? 0 : row;
+          const int dx = mn ? step : 0, dy = mn ? 0 : step;
+          const int kx = mn ? 0 : kFfnBK, ky = mn ? kFfnBK : 0;
+          // the next tile is wanted two rings before this one's end: taken earlier, it
+          // would wait here behind this one while other units run dry. Two ranges, so that
+          // the loop itself has nothing to ask.
+          const bool last = g + 1 == p.segments;
+          const int cut = !last ? k_blocks : k_blocks > 2 * kStages ? k_blocks - 2 * kStages : 0;
+          for (int kb = 0, end = cut;; ++kb) {
+            if (kb == end) {
+              if (take && leader && !of_b && last && end == cut) mbar_arrive(want_bar);
+              if (end == k_blocks) break;
+              end = k_blocks;
             }
-          } else {
-            brow0 = c.col0 + rank * 128;
-            brow1 = brow0 + 64;
-          }
-          for (int kb = 0; kb < p.k_blocks; ++kb) {
             if (!wait1(&empty_bar[stage], phase ^ 1u)) {
               ok = false;
               break;
             }
-            uint8_t* sa = tiles + stage * kFfnStageBytes;
-            uint8_t* sb = sa + kFfnTileBytes;
-            const uint32_t fb = PAIR ? mapa_shared(smem_addr(&full_bar[stage]), 0) : 0u;
-            if (leader)
-              mbar_arrive_expect_tx(&full_bar[stage], (PAIR ? 2u : 1u) * kFfnStageBytes);
-            const int k0 = kb * kFfnBK;
-            ffn_load<PAIR>(&p.a[g], amn, &full_bar[stage], fb, sa, arow, k0, pol);
-            ffn_load<PAIR>(&p.a[g], amn, &full_bar[stage], fb, sa + kFfnTileBytes / 2, arow + 64,
-                           k0, pol);
-            ffn_load<PAIR>(mb0, bmn, &full_bar[stage], fb, sb, brow0, k0, pol);
-            ffn_load<PAIR>(mb1, bmn, &full_bar[stage], fb, sb + kFfnTileBytes / 2, brow1, k0, pol);
+            uint8_t* to = tiles + stage * kFfnStageBytes + (of_b ? kFfnTileBytes : 0);
+            uint64_t* bar = &full_bar[stage];
+            const uint32_t fb = PAIR ? mapa_shared(smem_addr(bar), 0) : 0u;
+            // one arrival a phase, for the bytes of both operands (and CTAs): the others'
+            // copies may complete before it
+            if (leader && !of_b) mbar_arrive_expect_tx(bar, (PAIR ? 2u : 1u) * kFfnStageBytes);
+            ffn_load<PAIR>(m0, bar, fb, to, x, y, pol);
+            ffn_load<PAIR>(m1, bar, fb, to + kFfnTileBytes / 2, x + dx, y + dy, pol);
+            x += kx;
+            y += ky;
             issued_mask |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
             if (++stage == kStages) {
@@ -319,7 +371,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = unit; t < a.tiles && ok; t += units) {
+      for (int t = unit; ok && t >= 0; t = ok ? next_tile(t) : -1) {
         const FfnTile c = ffn_decode<EPI, SHAPE>(t, a);
         const FfnProduct& p = a.p[c.p];
         const bool amn = p.a_mn != 0, bmn = p.b_mn != 0;
@@ -366,6 +418,34 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       commit(done_bar);
       wait_drain(done_bar, 0);
     }
+  } else if (warp == 2 + kFfnEpiWarps) {
+    if (take && lane == 0 && leader) {
+      // ------------------------------------------------ tiles
+      const uint32_t ring_peer = PAIR ? mapa_shared(smem_addr(&tile_ring[0]), 1) : 0u;
+      const uint32_t full_peer = PAIR ? mapa_shared(smem_addr(&tr_full[0]), 1) : 0u;
+      int n = 0;
+      uint32_t want_ph = 0;
+      while (n >= 0) {
+        if (!wait1(want_bar, want_ph)) break;
+        want_ph ^= 1u;
+        if (!wait1(&tr_empty[ring_slot], ring_ph ^ 1u)) break;
+        n = units + atomicAdd(a.counter, 1);
+        if (n >= a.tiles) n = -1;
+        tile_ring[ring_slot] = n;
+        if constexpr (PAIR) st_cluster_s32(ring_peer + 4u * static_cast<uint32_t>(ring_slot), n);
+        mbar_arrive(&tr_full[ring_slot]);
+        if constexpr (PAIR) mbar_arrive_cluster(full_peer + 8u * static_cast<uint32_t>(ring_slot));
+        if (++ring_slot == kFfnRing) {
+          ring_slot = 0;
+          ring_ph ^= 1u;
+        }
+      }
+      if (atomicAdd(a.counter + 1, 1) == units - 1) {
+        // every unit has taken its last tile: ready for the next launch
+        a.counter[0] = 0;
+        a.counter[1] = 0;
+      }
+    }
   } else {
     // ------------------------------------------------ epilogue
     const int quarter = warp & 3;
@@ -380,7 +460,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     uint32_t bar_ph = 0;     // bit s: parity of slot s's next load
     uint32_t in_flight = 0;  // lane 0: slots with a load that nobody has waited for
     int turn = 0;            // slot of the next chunk
-    for (int t = unit; t < a.tiles; t += units) {
+    auto next_of_warp = [&](int t) {
+      if (!take) return next_tile(t);
+      if (lane == 0) t = next_tile(t);
+      return __shfl_sync(0xffffffffu, t, 0);
+    };
+    for (int t = unit; t >= 0; t = next_of_warp(t)) {
       const FfnTile c = ffn_decode<EPI, SHAPE>(t, a);
       const FfnProduct& p = a.p[c.p];
       const int row = c.row0 + rank * 128 + quarter * 32;
