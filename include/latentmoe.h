@@ -698,7 +698,7 @@ int latentmoe_ffn_destroy(latentmoe_ffn_t h);
 
 /* ---- RMS norm with the residual's addition. ------------------------------
  * What stands between a residual stream and the layer (or the gated block
- * below), and its gradient. The pages give no formula; it is the usual one. For
+ * above), and its gradient. The pages give no formula; it is the usual one. For
  * T tokens of width d:
  *
  *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd weight
@@ -731,7 +731,7 @@ typedef struct {
 /* One launch, asynchronous on `stream`, on the current device; no handle, no
  * scratch, bitwise reproducible, capturable. T >= 1, 1 <= d <= 16384. Rows of
  * numbers beyond 1.8e19, whose squares fp32 cannot hold, come out right; a NaN
- * makes its own row NaN. Errors: INVALID_ARG (NULL x or weight, neither y nor
+ * makes its own row NaN, an infinity its own entry, with zeros in the rest of the row. Errors: INVALID_ARG (NULL x or weight, neither y nor
  * codes, codes without scales, sum without residual, sizes, ld < d, an unknown
  * type or scale_block, eps), UNSUPPORTED (d > 16384, T >= 2^31, an fp32 x with a
  * bf16 residual, a pointer not aligned to its type), CUDA. */

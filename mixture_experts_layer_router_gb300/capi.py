@@ -1,8 +1,8 @@
 """ctypes binding of liblatentmoe.so (include/latentmoe.h), same names.
 
-Argument marshalling only: every step of the layer, and of the training
-operators (balance loss, router backward, Muon), runs in the library's CUDA
-kernels. PyTorch provides device memory (``tensor.data_ptr()``) and
+Argument marshalling only: every step of the layer, of the training operators
+(balance loss, router backward, Muon) and of the block around it (RMS norm,
+gated feed-forward block, gradient clipping) runs in the library's CUDA kernels. PyTorch provides device memory (``tensor.data_ptr()``) and
 streams (``torch.cuda.current_stream().cuda_stream``). There is no fallback:
 ``load()`` raises if the library is missing or cannot be loaded.
 """
@@ -752,10 +752,12 @@ class GatedFFN:
 
     def __init__(self, d: int, F: int, max_tokens: int = 1, training: bool = False):
         self.dims = latentmoe_ffn_dims(d, F, max_tokens, int(training))
+        self.device = None
         h = _c_void_p()
         check(load().latentmoe_ffn_create(ctypes.byref(self.dims), ctypes.byref(h)),
               "latentmoe_ffn_create")
         self.handle = h
+        self.device = _device()
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
@@ -783,6 +785,7 @@ class GatedFFN:
 
     def _weights(self, w_g, w_u, w_d):
         d, F = self.dims.hidden, self.dims.ffn
+        _need(_device() == self.device, "the handle belongs to another device than the current one")
         return latentmoe_ffn_weights(self._matrix(w_g, "w_g", F, d), self._matrix(w_u, "w_u", F, d),
                                      self._matrix(w_d, "w_d", d, F))
 
