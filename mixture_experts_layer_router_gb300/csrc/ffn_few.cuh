@@ -15,6 +15,12 @@
 // have left an SM (programmatic dependent launch), and wait for the whole of it only
 // before they read h.
 //
+// What bounds it: DRAM, and for small weights the two launches' ends (last loads, parts
+// to memory, last arrival, sums: about 5 us each, more with more tokens). 8704 x 10240, one
+// token 88 us (6.1 TB/s, 0.90 of the copy rate), 27 tokens 95, 64 tokens 107, 128 tokens 128;
+// 2048 x 2048, one token 14. Taking the tile from a unit's number by division in the
+// producing thread cost 11 us of 105, a ring of 6 stages in place of 11 another 4.
+//
 //   warp 0      TMA producer (one lane)
 //   warp 1      TMEM allocator, MMA issuer (one lane)
 //   warps 2..5  epilogue (TMEM lane quarter warp % 4)

@@ -13,6 +13,12 @@
 // fp32 cannot hold (a thread's sum of a tile above 2^96 or below 2^-80) are added
 // in 64 bits throughout, so the norm is right for any finite numbers. The order of
 // the additions depends on the tensors' sizes and alignment alone.
+//
+// What bounds it: DRAM, the gradients being read twice: 330M bf16 numbers 310 us (2 x 660
+// MB read, 660 written: 6.4 TB/s), of which the norm is 98 (6.7 TB/s; 174 while the pieces
+// went through local memory). 2M x 3 tensors 12 us, 14 of 450,000 in all 8 us, latency.
+// Pieces a thread 4 / 8 (us): 330M 321 / 310, 6M 16 / 12. 64-bit square roots and divisions
+// in one thread a CTA and not in all took 6M from 29 to 16.
 #include <string.h>
 
 #include "grads.h"
