@@ -678,15 +678,15 @@ int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, con
                           int64_t ld_x, void* y, int64_t ld_y, void* gate, void* up, int64_t T,
                           latentmoe_stream_t stream);
 
-/* The gradient, in 2 launches (3 for fewer than 8 tokens). Needs a handle made with
+/* The gradient, in 2 launches (up to 4 for few tokens). Needs a handle made with
  * `training`; otherwise as the forward. Also UNSUPPORTED: `accumulate` with bf16
  * gradients. */
 int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
                            const latentmoe_ffn_grad* g, int64_t T, latentmoe_stream_t stream);
 
 /* Tiles of the products: 0 = 128 x 128 on single SMs, 1 = 256 x 256 on SM pairs, 2
- * (the default) = whichever is expected to take the least time; the forward then has a
- * kernel of its own for few tokens, which 3 asks for (up to 128 tokens; otherwise as 2). */
+ * (the default) = whichever is expected to take the least time; few tokens then
+ * have a kernel of their own, which 3 asks for (up to 128 tokens; otherwise as 2). */
 int latentmoe_ffn_set_sm_pairs(latentmoe_ffn_t h, int mode);
 
 /* As latentmoe_get_status, latentmoe_get_launch_count, latentmoe_last_cuda_error

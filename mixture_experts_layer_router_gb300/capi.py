@@ -859,7 +859,7 @@ class GatedFFN:
 
     def set_sm_pairs(self, mode: int) -> None:
         """0: 128 x 128 tiles on single SMs; 1: 256 x 256 on SM pairs; 2: automatic;
-        3: the forward's kernel for few tokens."""
+        3: the kernel for few tokens."""
         self._check(load().latentmoe_ffn_set_sm_pairs(self.handle, int(mode)),
                     "latentmoe_ffn_set_sm_pairs")
 

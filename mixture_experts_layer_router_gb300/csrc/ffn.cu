@@ -127,7 +127,7 @@ double plan(FfnArgs& a, int epi, int shape, int sms) {
   const bool pair = shape == lmoe::kFfnPair;
   const int cols = epi == lmoe::kFfnGateUp ? lmoe::ffn_bn(shape) / 2 : lmoe::ffn_bn(shape);
   const long long units = pair ? sms / 2 : sms;
-  const double block = pair ? 310.0 : 320.0, least = pair ? 2000.0 : 1000.0;
+  const double block = pair ? 310.0 : 320.0, least = pair ? 1850.0 : 1300.0;
   const double end = !pair ? 0.0 : epi == lmoe::kFfnDGate ? 4000.0 : 1500.0;
   long long tiles = 0;
   double work = 0.0, longest = 0.0;
@@ -195,31 +195,92 @@ bool few_wins(const latentmoe_ffn* h, long long T) {
   return few < tiles;
 }
 
-// One product for few tokens: out [T, rows] of x [T, K] and weights [rows, K].
-int run_few(latentmoe_ffn* h, int epi, const Mat& x, const void* w0, const void* w1, long long rows,
-            bool early, void* out, long long ld, void* gate, void* up, cudaStream_t s) {
+// Whether the gradient of T tokens takes it for dgate and dx (dW then goes alone): up to 24
+// tokens, for weights that take longer to read than the launch that it adds. us, few /
+// tiles, with dx alone and with everything: 8704 x 10240 8 tokens 93 / 137 and 214 / 235, 64
+// tokens 120 / 140 and 262 / 236; 4096 x 2048 16 tokens 28 / 53 and 44 / 61, 32 tokens 38 / 44
+// and 60 / 50; 2048 x 2048 17 tokens 25 / 34 and 35 / 39, 32 tokens 30 / 34 and 42 / 35; 1024 x
+// 1024 8 tokens 14 / 20 and 20 / 21; 256 x 256 8 tokens 11 / 12 and 15 / 12.
+bool dgate_few_wins(const latentmoe_ffn* h, long long T) {
+  return T <= 24 && h->d * h->F >= (1ll << 21);
+}
+
+// What the products for few tokens have in common; x is their one operand or first one.
+bool few_args(lmoe::FewArgs* a, const latentmoe_ffn* h, int epi, const Mat& x, long long rows,
+              long long k_blocks) {
+  memset(a, 0, sizeof(*a));
+  a->tokens = static_cast<int>(x.rows);
+  a->rows = static_cast<int>(rows);
+  a->tiles = static_cast<int>(ceil_div(rows, epi == lmoe::kFfnGateUp ? 64 : 128));
+  a->k_blocks = static_cast<int>(k_blocks);
+  a->cut = a->k_blocks;
+  a->parts = h->parts;
+  a->arrived = h->arrived;
+  a->status = h->status;
+  return encode(&a->x[0], x.p, x.rows, x.cols, x.ld, 64, lmoe::few_tokens(a->tokens), false);
+}
+
+int run_few(latentmoe_ffn* h, int epi, bool transposed, const lmoe::FewArgs& a, cudaStream_t s) {
   const lmoe::PdlScope pdl(true);
-  lmoe::FewArgs a;
-  memset(&a, 0, sizeof(a));
-  a.tokens = static_cast<int>(x.rows);
-  a.rows = static_cast<int>(rows);
-  a.tiles = static_cast<int>(ceil_div(rows, epi == lmoe::kFfnGateUp ? 64 : 128));
-  a.k_blocks = static_cast<int>(ceil_div(x.cols, lmoe::kFfnBK));
-  a.early = early ? 1 : 0;
-  a.parts = h->parts;
-  a.arrived = h->arrived;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.gate = static_cast<__nv_bfloat16*>(gate);
-  a.up = static_cast<__nv_bfloat16*>(up);
-  a.ld = ld;
-  a.status = h->status;
-  const Mat w = {w0, rows, x.cols, x.cols}, v = {w1, rows, x.cols, x.cols};
-  if (!operand(&a.w[0], w) || (w1 != nullptr && !operand(&a.w[1], v)) ||
-      !encode(&a.x, x.p, x.rows, x.cols, x.ld, 64, lmoe::few_tokens(a.tokens), false))
-    return LATENTMOE_ERR_CUDA;
-  FFN_CK(h, lmoe::launch_ffn_few(epi, a, h->sms, s));
+  FFN_CK(h, lmoe::launch_ffn_few(epi, transposed, a, h->sms, s));
   h->launches += 1;
   return LATENTMOE_OK;
+}
+
+// The forward for few tokens.
+int forward_few(latentmoe_ffn* h, const latentmoe_ffn_weights* w, const Mat& x, void* y,
+                long long ld_y, void* gate, void* up, cudaStream_t s) {
+  const long long d = h->d, F = h->F, T = x.rows;
+  lmoe::FewArgs a;
+  if (!few_args(&a, h, lmoe::kFfnGateUp, x, F, ceil_div(d, lmoe::kFfnBK)) ||
+      !operand(&a.w[0], {w->w_g, F, d, d}) || !operand(&a.w[1], {w->w_u, F, d, d}))
+    return LATENTMOE_ERR_CUDA;
+  a.out = h->h;
+  a.ld = F;
+  a.gate = static_cast<__nv_bfloat16*>(gate);
+  a.up = static_cast<__nv_bfloat16*>(up);
+  const int rc = run_few(h, lmoe::kFfnGateUp, false, a, s);
+  if (rc != LATENTMOE_OK) return rc;
+  if (!few_args(&a, h, lmoe::kFfnPlain, {h->h, T, F, F}, d, ceil_div(F, lmoe::kFfnBK)) ||
+      !operand(&a.w[0], {w->w_d, d, F, F}))
+    return LATENTMOE_ERR_CUDA;
+  a.early = 1;
+  a.out = static_cast<__nv_bfloat16*>(y);
+  a.ld = ld_y;
+  return run_few(h, lmoe::kFfnPlain, false, a, s);
+}
+
+// dg, du and h for few tokens.
+int dgate_few(latentmoe_ffn* h, const void* w_d, const Mat& dy, const void* gate, const void* up,
+              cudaStream_t s) {
+  const long long d = h->d, F = h->F;
+  lmoe::FewArgs a;
+  if (!few_args(&a, h, lmoe::kFfnDGate, dy, F, ceil_div(d, lmoe::kFfnBK)) ||
+      !operand(&a.w[0], {w_d, d, F, F}))
+    return LATENTMOE_ERR_CUDA;
+  a.out = h->dg;
+  a.du = h->du;
+  a.h = h->h;
+  a.ld = F;
+  a.gate = static_cast<__nv_bfloat16*>(const_cast<void*>(gate));
+  a.up = static_cast<__nv_bfloat16*>(const_cast<void*>(up));
+  return run_few(h, lmoe::kFfnDGate, true, a, s);
+}
+
+// dx for few tokens, after the launch that leaves dg and du.
+int dx_few(latentmoe_ffn* h, const latentmoe_ffn_weights* w, long long T, void* dx, long long ld_dx,
+           cudaStream_t s) {
+  const long long d = h->d, F = h->F, blocks = ceil_div(F, lmoe::kFfnBK);
+  lmoe::FewArgs a;
+  if (!few_args(&a, h, lmoe::kFfnPlain, {h->dg, T, F, F}, d, 2 * blocks) ||
+      !encode(&a.x[1], h->du, T, F, F, 64, lmoe::few_tokens(static_cast<int>(T)), false) ||
+      !operand(&a.w[0], {w->w_g, F, d, d}) || !operand(&a.w[1], {w->w_u, F, d, d}))
+    return LATENTMOE_ERR_CUDA;
+  a.cut = static_cast<int>(blocks);
+  a.early = 1;
+  a.out = static_cast<__nv_bfloat16*>(dx);
+  a.ld = ld_dx;
+  return run_few(h, lmoe::kFfnPlain, true, a, s);
 }
 
 bool stride(int64_t* ld, int64_t width) {
@@ -317,11 +378,7 @@ int latentmoe_ffn_forward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w, con
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
   const long long d = h->d, F = h->F;
   if (h->mode == 3 ? T <= lmoe::kFewMost : h->mode == 2 && few_wins(h, T)) {
-    const int rc = run_few(h, lmoe::kFfnGateUp, {x, T, d, ld_x}, w->w_g, w->w_u, F, false, h->h, F,
-                           gate, up, s);
-    if (rc != LATENTMOE_OK) return rc;
-    return run_few(h, lmoe::kFfnPlain, {h->h, T, F, F}, w->w_d, nullptr, d, true, y, ld_y, nullptr,
-                   nullptr, s);
+    return forward_few(h, w, {x, T, d, ld_x}, y, ld_y, gate, up, s);
   }
   Launch l(h);
   FfnProduct& p = l.add({x, T, d, ld_x}, false, {w->w_g, F, d, d}, false, T, F, d);
@@ -376,20 +433,32 @@ int latentmoe_ffn_backward(latentmoe_ffn_t h, const latentmoe_ffn_weights* w,
     x = {h->xs, R, d, d};
   }
   const Mat hm = {h->h, R, F, F}, dg = {h->dg, R, F, F}, du = {h->du, R, F, F};
-  Launch l(h);
-  FfnProduct& p = l.add(dy, false, {w->w_d, d, F, F}, true, T, F, d);
-  l.ok = l.ok && chunk(&l.a.gate, {g.gate, T, F, F}) && chunk(&l.a.up, {g.up, T, F, F}) &&
-         chunk(&p.out[0], {h->dg, T, F, F}) && chunk(&p.out[1], {h->du, T, F, F}) &&
-         chunk(&p.out[2], {h->h, T, F, F});
-  const int rc = run(h, l, lmoe::kFfnDGate, s);
+  const bool few = h->mode == 3 ? T <= lmoe::kFewMost : h->mode == 2 && dgate_few_wins(h, T);
+  int rc;
+  if (few) {
+    rc = dgate_few(h, w->w_d, {dy.p, T, d, dy.ld}, g.gate, g.up, s);
+  } else {
+    Launch l(h);
+    FfnProduct& p = l.add(dy, false, {w->w_d, d, F, F}, true, T, F, d);
+    l.ok = l.ok && chunk(&l.a.gate, {g.gate, T, F, F}) && chunk(&l.a.up, {g.up, T, F, F}) &&
+           chunk(&p.out[0], {h->dg, T, F, F}) && chunk(&p.out[1], {h->du, T, F, F}) &&
+           chunk(&p.out[2], {h->h, T, F, F});
+    rc = run(h, l, lmoe::kFfnDGate, s);
+  }
   if (rc != LATENTMOE_OK) return rc;
+  const bool dx_apart = g.dx != nullptr && few;
+  if (dx_apart) {
+    rc = dx_few(h, w, T, g.dx, g.ld_dx, s);
+    if (rc != LATENTMOE_OK || (g.dw_g == nullptr && g.dw_u == nullptr && g.dw_d == nullptr))
+      return rc;
+  }
   Launch m(h);
   const bool f32 = g.dw_dtype == LATENTMOE_FP32;
   const int out_mode = !f32             ? lmoe::kFfnBf16
                        : g.accumulate ? lmoe::kFfnF32Add
                                       : lmoe::kFfnF32;
   auto add_dx = [&]() {
-    if (g.dx == nullptr) return;
+    if (g.dx == nullptr || dx_apart) return;
     FfnProduct& q = m.add(dg, false, {w->w_g, F, d, d}, true, T, d, F);
     q.segments = 2;
     m.ok = m.ok && operand(&q.a[1], du) && operand(&q.b[1], {w->w_u, F, d, d}) &&

@@ -50,8 +50,8 @@ cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream
 
 // Operands of fewer than kFfnLeastRows rows, padded: a TMA load of a box of a matrix
 // with fewer than 8 rows (the height of a swizzle pattern) takes several times as long
-// as of one with 8, most of them outside alike. 8704 x 10240, 4 tokens: backward 545 us,
-// with padding 319; 8 tokens 319. xs, dys [8, d] = x and dy [tokens, d] (x null: none),
+// as of one with 8, most of them outside alike. 8704 x 10240 on tiles, 4 tokens: backward
+// 545 us, with padding 319; 8 tokens 319. xs, dys [8, d] = x and dy [tokens, d] (x null: none),
 // rows of h, dg and du from `tokens` to 8: zeros.
 constexpr int kFfnLeastRows = 8;
 cudaError_t launch_ffn_pad(const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* dy,
@@ -59,21 +59,27 @@ cudaError_t launch_ffn_pad(const __nv_bfloat16* x, long long ld_x, const __nv_bf
                            __nv_bfloat16* dys, __nv_bfloat16* h, __nv_bfloat16* dg,
                            __nv_bfloat16* du, cudaStream_t s);
 
-// Few tokens: D^T = W x^T with 128 rows of weights by up to 128 tokens a tile
-// (ffn_few.cuh). kFfnGateUp (64 features a tile) or kFfnPlain.
+// Few tokens: D^T = W x^T with 128 rows of W by up to 128 tokens a tile (ffn_few.cuh).
+//   kFfnGateUp  W = Wg and Wu, 64 rows of each a tile: h, gate, up
+//   kFfnPlain   W = Wd: y; or, from the transposes, W = Wg^T and then Wu^T with x = dg and
+//               then du: dx
+//   kFfnDGate   W = Wd^T, x = dy: dg, du, h
 constexpr int kFewMost = 128;      // tokens
 constexpr int kFewLeast = 8;       // k-blocks of a part, unless a tile has fewer
 struct FewArgs {
-  CUtensorMap w[2];  // gate+up: gate and up; plain: w[0]; boxes of 64 x 64
-  CUtensorMap x;     // [tokens, K]; boxes of 64 columns x few_tokens(tokens) rows
+  CUtensorMap w[2];  // boxes of 64 x 64 of the matrix in memory
+  CUtensorMap x[2];  // [tokens, K]; boxes of 64 columns x few_tokens(tokens) rows
   int tokens;
   int rows;          // output features
   int tiles, k_blocks;
+  int cut;           // k-blocks of w[0] and x[0] (transposed; else k_blocks)
   int early;         // weights may be loaded before the kernel ahead has finished
   float* parts;      // [CTAs, 2, few_tokens, 128]
   int* arrived;      // [tiles], zero; left zero
-  __nv_bfloat16* out;   // h or y, [tokens, ld]
-  __nv_bfloat16* gate;  // or null; [tokens, rows]
+  __nv_bfloat16* out;   // [tokens, ld]: h, y, dx or dg
+  __nv_bfloat16* du;    // kFfnDGate: [tokens, ld], and h
+  __nv_bfloat16* h;
+  __nv_bfloat16* gate;  // [tokens, rows]; kFfnGateUp: written, or null; kFfnDGate: read
   __nv_bfloat16* up;
   long long ld;
   unsigned* status;
@@ -83,6 +89,7 @@ inline int few_tokens(int tokens) {
 }
 // CTAs of a launch: one an SM, fewer where parts would get too short.
 int few_ctas(int tiles, int k_blocks, int sms);
-cudaError_t launch_ffn_few(int epi, const FewArgs& a, int sms, cudaStream_t s);
+// transposed: W lies as [K, rows] in memory (kFfnPlain, kFfnDGate).
+cudaError_t launch_ffn_few(int epi, bool transposed, const FewArgs& a, int sms, cudaStream_t s);
 
 }  // namespace lmoe

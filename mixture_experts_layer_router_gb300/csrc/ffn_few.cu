@@ -11,36 +11,38 @@ int few_ctas(int tiles, int k_blocks, int sms) {
   return static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
 }
 
-template <int EPI, int NT>
+template <int EPI, int NT, bool MN>
 static cudaError_t launch_few_impl(const FewArgs& a, int sms, cudaStream_t s) {
   static bool smem_set[kMaxDevices] = {};
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!smem_set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(ffn_few_kernel<EPI, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(ffn_few_kernel<EPI, NT, MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              few_smem_bytes(NT));
     if (e != cudaSuccess) return e;
     smem_set[dev] = true;
   }
-  return launch_kernel(ffn_few_kernel<EPI, NT>,
+  return launch_kernel(ffn_few_kernel<EPI, NT, MN>,
                        dim3(static_cast<unsigned>(few_ctas(a.tiles, a.k_blocks, sms))),
                        dim3(kFewThreads), few_smem_bytes(NT), s, 1, false, a);
 }
 
-template <int EPI>
+template <int EPI, bool MN>
 static cudaError_t launch_few_tokens(const FewArgs& a, int sms, cudaStream_t s) {
   switch (few_tokens(a.tokens)) {
-    case 16: return launch_few_impl<EPI, 16>(a, sms, s);
-    case 32: return launch_few_impl<EPI, 32>(a, sms, s);
-    case 64: return launch_few_impl<EPI, 64>(a, sms, s);
-    default: return launch_few_impl<EPI, 128>(a, sms, s);
+    case 16: return launch_few_impl<EPI, 16, MN>(a, sms, s);
+    case 32: return launch_few_impl<EPI, 32, MN>(a, sms, s);
+    case 64: return launch_few_impl<EPI, 64, MN>(a, sms, s);
+    default: return launch_few_impl<EPI, 128, MN>(a, sms, s);
   }
 }
 
-cudaError_t launch_ffn_few(int epi, const FewArgs& a, int sms, cudaStream_t s) {
-  return epi == kFfnGateUp ? launch_few_tokens<kFfnGateUp>(a, sms, s)
-                           : launch_few_tokens<kFfnPlain>(a, sms, s);
+cudaError_t launch_ffn_few(int epi, bool transposed, const FewArgs& a, int sms, cudaStream_t s) {
+  if (epi == kFfnGateUp) return launch_few_tokens<kFfnGateUp, false>(a, sms, s);
+  if (epi == kFfnDGate) return launch_few_tokens<kFfnDGate, true>(a, sms, s);
+  return transposed ? launch_few_tokens<kFfnPlain, true>(a, sms, s)
+                    : launch_few_tokens<kFfnPlain, false>(a, sms, s);
 }
 
 }  // namespace lmoe

@@ -3,7 +3,8 @@
 // for that alone.
 //
 // D^T = W x^T: 128 rows of weights are the MMA's M (gate+up: 64 gate rows and the up
-// rows of the same features), the tokens its N, so no lane of the tensor core waits
+// rows of the same features; in the gradient, columns of the weights, an MN-major
+// operand), the tokens its N, so no lane of the tensor core waits
 // for tokens that are not there. The k-blocks of all tiles form one sequence that is
 // cut into equal parts, one a CTA, wherever the cuts fall: every SM reads the same
 // number of weights (a tile a CTA would leave 8704 rows / 128 = 68 tiles on 152 SMs).
@@ -101,7 +102,7 @@ __device__ __forceinline__ void few_sum(const float* parts, long long part, int 
   }
 }
 
-template <int EPI, int NT>
+template <int EPI, int NT, bool MN>
 __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kStages = few_stages(NT);
   constexpr int kStage = few_stage_bytes(NT);
@@ -157,6 +158,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
     if (EPI == kFfnGateUp) {
       tma_load_2d(&a.w[0], &full_bar[stage], dst, k0, tile * 64, pol);
       tma_load_2d(&a.w[1], &full_bar[stage], dst + kFewWBytes / 2, k0, tile * 64, pol);
+    } else if (MN) {
+      const bool second = kb >= a.cut;
+      const CUtensorMap* map = second ? &a.w[1] : &a.w[0];
+      const int row = second ? k0 - a.cut * kFfnBK : k0;
+      tma_load_2d(map, &full_bar[stage], dst, tile * 128, row, pol);
+      tma_load_2d(map, &full_bar[stage], dst + kFewWBytes / 2, tile * 128 + 64, row, pol);
     } else {
       tma_load_2d(&a.w[0], &full_bar[stage], dst, k0, tile * 128, pol);
       tma_load_2d(&a.w[0], &full_bar[stage], dst + kFewWBytes / 2, k0, tile * 128 + 64, pol);
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
       // ------------------------------------------------ TMA producer
       tma_prefetch_desc(&a.w[0]);
       if (EPI == kFfnGateUp) tma_prefetch_desc(&a.w[1]);
-      tma_prefetch_desc(&a.x);
+      tma_prefetch_desc(&a.x[0]);
       const uint64_t pol = policy_evict_first(), pol_x = policy_evict_last();
       // the units in turn: a division for each would take as long as its copies
       int tile = static_cast<int>(u0 / a.k_blocks);
@@ -192,7 +199,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
           if (!wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag, a.status)) break;
           next_w(stage);
         }
-        tma_load_2d(&a.x, &full_bar[stage], ring + stage * kStage + kFewWBytes, x_kb * kFfnBK, 0,
+        const bool second = MN && x_kb >= a.cut;
+        tma_load_2d(second ? &a.x[1] : &a.x[0], &full_bar[stage],
+                    ring + stage * kStage + kFewWBytes, (second ? x_kb - a.cut : x_kb) * kFfnBK, 0,
                     pol_x);
         if (++x_kb == a.k_blocks) x_kb = 0;
         issued_mask |= 1u << stage;
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
     pdl_wait();
     if (lane == 0) {
       // ------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = instr_desc_bf16(128, NT);
+      constexpr uint32_t idesc = instr_desc_bf16(128, NT) | (MN ? 1u << 15 : 0u);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -229,11 +238,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
             break;
           }
           tc_fence_after_sync();
-          const uint64_t dw = smem_desc_sw128(ring + stage * kStage);
+          const uint64_t dw =
+              MN ? ffn_desc_mn(ring + stage * kStage) : smem_desc_sw128(ring + stage * kStage);
           const uint64_t dx = smem_desc_sw128(ring + stage * kStage + kFewWBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            tc_mma(d_tmem, dw + 2ull * k, dx + 2ull * k, idesc, accum);
+            tc_mma(d_tmem, dw + (MN ? 128ull : 2ull) * k, dx + 2ull * k, idesc, accum);
             accum = 1u;
           }
           tc_commit(&empty_bar[stage]);
@@ -324,8 +334,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) ffn_few_kernel(const __grid_co
               float s[1][kFewBatch];
               few_sum(a.parts, NT * 128, c0, c1, a.tokens, n, 1, one, s);
 #pragma unroll
-              for (int j = 0; j < kFewBatch; ++j)
-                if (n + j < a.tokens) a.out[(n + j) * a.ld + f] = __float2bfloat16_rn(s[0][j]);
+              for (int j = 0; j < kFewBatch; ++j) {
+                const long long t = n + j;
+                if (t >= a.tokens) break;
+                if (EPI == kFfnDGate) {
+                  const float g = __bfloat162float(a.gate[t * a.rows + f]);
+                  const float u = __bfloat162float(a.up[t * a.rows + f]);
+                  const float sig = ffn_sigmoid(g), act = g * sig;
+                  a.out[t * a.ld + f] =
+                      __float2bfloat16_rn(s[0][j] * u * fmaf(act, 1.0f - sig, sig));
+                  a.du[t * a.ld + f] = __float2bfloat16_rn(s[0][j] * act);
+                  a.h[t * a.ld + f] = __float2bfloat16_rn(act * u);
+                } else {
+                  a.out[t * a.ld + f] = __float2bfloat16_rn(s[0][j]);
+                }
+              }
             }
           }
         }

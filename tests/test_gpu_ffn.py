@@ -6,7 +6,10 @@ rounded to bf16 before the next product: half a step, R = 2^-8, of an entry (wit
 the activation's own error, a few 2^-22, far below it). So for D = A B^T with A so
 rounded, entry by entry,
     |D - exact| <= R |exact| + ((1 + R) R + 2^-16 + (K + 4) 2^-24) (|A| |B|^T),
-the first term being the result's own rounding (0 in fp32). That worst case grows
+the first term being the result's own rounding (0 in fp32). dh is such a sum itself,
+without a rounding: it is off by E = (d + 4) 2^-24 |dy| |Wd|, however small it comes out
+where its terms cancel, and dg and du by |up SiLU'| E and |SiLU| E, which |B| then passes
+on (one token's dW has nothing to average that out). That worst case grows
 with K where the roundings in fact cancel; so results of 1000 entries or more are
 also held to it in the mean square: two independent roundings of at most R / sqrt(3)
 each, 3.2e-3 of the result's norm, TOL = 4e-3 (fp32 results: one, 2.3e-3, the same
@@ -45,25 +48,28 @@ def formula(x, w):
 
 
 def gradients(dy, x, gate, up, w):
-    """name -> (exact, magnitudes |A| |B|^T, K)."""
+    """name -> (exact, magnitudes |A| |B|^T, K, what dh is off by, passed on)."""
     dy, x, g, u = (t.double() for t in (dy, x, gate, up))
     wg, wu, wd = (w[n].double() for n in ("w_g", "w_u", "w_d"))
     T, F = g.shape
     s = torch.sigmoid(g)
-    dh = dy @ wd
-    dg, du, h = dh * u * (s + g * s * (1 - s)), dh * g * s, g * s * u
-    return {"dx": (dg @ wg + du @ wu, dg.abs() @ wg.abs() + du.abs() @ wu.abs(), 2 * F),
-            "dw_g": (dg.T @ x, dg.abs().T @ x.abs(), T), "dw_u": (du.T @ x, du.abs().T @ x.abs(), T),
-            "dw_d": (dy.T @ h, dy.abs().T @ h.abs(), T),
-            # what dh itself is off by, (d + 4) 2^-24 of |dy| |Wd|, is in the 2^-16
-            }
+    dh, off = dy @ wd, (dy.shape[1] + 4) * 2.0 ** -24 * (dy.abs() @ wd.abs())
+    slope, act = u * (s + g * s * (1 - s)), g * s
+    dg, du, h = dh * slope, dh * act, act * u
+    og, ou = off * slope.abs(), off * act.abs()
+    zero = torch.zeros((), device="cuda", dtype=torch.float64)
+    return {"dx": (dg @ wg + du @ wu, dg.abs() @ wg.abs() + du.abs() @ wu.abs(), 2 * F,
+                   og @ wg.abs() + ou @ wu.abs()),
+            "dw_g": (dg.T @ x, dg.abs().T @ x.abs(), T, og.T @ x.abs()),
+            "dw_u": (du.T @ x, du.abs().T @ x.abs(), T, ou.T @ x.abs()),
+            "dw_d": (dy.T @ h, dy.abs().T @ h.abs(), T, zero)}
 
 
-def check(got, exact, size, K, out=BF16):
+def check(got, exact, size, K, passed=0.0, out=BF16):
     slack = (1 + R) * R + 2.0 ** -16 + (K + 4) * 2.0 ** -24
     own = R if out == BF16 else 2.0 ** -24
     d = (got.double() - exact).abs()
-    assert bool((d <= own * exact.abs() + slack * size + 1e-30).all()), float((d / (slack * size + 1e-30)).max())
+    assert bool((d <= own * exact.abs() + slack * size + (1 + R) ** 2 * passed + 1e-30).all()), float((d / (slack * size + 1e-30)).max())
     if got.numel() >= 1000:
         assert float(d.norm()) <= TOL * float(exact.norm())
 
@@ -100,8 +106,8 @@ def test_forward(T, d, F, mode):
     assert m.status() == 0
 
 
-@pytest.mark.parametrize("mode", [0, 1, 2])
-@pytest.mark.parametrize("T,d,F", SIZES)
+@pytest.mark.parametrize("mode", [0, 1, 2, 3])
+@pytest.mark.parametrize("T,d,F", SIZES + FEW)
 def test_backward(T, d, F, mode):
     gh.lib()
     x, w = block(T, d, F, seed=T + d + F)
@@ -111,8 +117,8 @@ def test_backward(T, d, F, mode):
     got = m.backward(dy, x, gate, up, **w)
     assert m.status() == 0
     want = gradients(dy, x, gate, up, w)
-    for n, (exact, size, K) in want.items():
-        check(got[n], exact, size, K)
+    for n in want:
+        check(got[n], *want[n])
     again = m.backward(dy, x, gate, up, **w)
     assert all(torch.equal(again[n], got[n]) for n in got)
     f32 = m.backward(dy, x, gate, up, **w, dw_dtype=F32)
@@ -143,8 +149,8 @@ def test_extreme_gates():
     gate[2] = 0.0
     m = capi.GatedFFN(d, F, max_tokens=T, training=True)
     got = m.backward(dy, x, gate, up, **w)
-    for n, (exact, size, K) in gradients(dy, x, gate, up, w).items():
-        check(got[n], exact, size, K)
+    for n, want in gradients(dy, x, gate, up, w).items():
+        check(got[n], *want)
     x = x * 100
     g, u, h, y = formula(x, w)
     check(m.forward(x, **w), y, h.abs() @ w["w_d"].double().abs().T, F)
@@ -174,7 +180,7 @@ def test_rows_of_wider_tensors_and_fewer_than_the_most():
     bdy, vdy = wide(dy)
     by, vy = wide(torch.zeros((T, d)))
     bdx, vdx = wide(torch.zeros((T, d)))
-    for mode in (0, 1, 2):
+    for mode in (0, 1, 2, 3):
         m.set_sm_pairs(mode)
         first.set_sm_pairs(mode)
         m.forward(vx, **w, out=vy)
