@@ -38,8 +38,8 @@ __device__ __forceinline__ float norm_scale(float top) {
 // Pieces a thread, and CTAs an SM that the registers are cut for. 16384 x 6656 to E4M3
 // by blocks / to bf16 (us): one piece, 832 threads, 2 CTAs 162 / 149; two pieces, 416
 // threads, 2 / 3 / 4 CTAs 165 / 135 / 145 and 146 / 126 / 143; four pieces 192 / 150.
-constexpr int norm_threads(int vpt) { return vpt == 1 ? 1024 : 512; }
-constexpr int norm_ctas(int vpt) { return vpt == 1 ? 2 : vpt == 2 ? 3 : 2; }
+constexpr int norm_threads(int vpt) { return vpt == 1 ? 128 : 512; }
+constexpr int norm_ctas(int vpt) { return vpt == 1 ? 12 : vpt == 2 ? 3 : 2; }
 
 template <typename XT, typename RT, bool RES, bool VEC, int VPT>
 __global__ void __launch_bounds__(norm_threads(VPT), norm_ctas(VPT)) rms_norm_kernel(const NormArgs a) {

@@ -11,21 +11,49 @@
 //
 // What bounds it: an iteration's latency (loads, one barrier, stores) with the rows that
 // the registers let an SM have on their way beside dw. 8192 x 6656, fp32 stream 161 us
-// (4.7 TB/s), 16384 x 6656, bf16 182 us (4.8), 16384 x 1024, fp32 44 us (5.3), 4096 x 2048,
-// bf16 20 us with both launches. Tried: the next row in registers (fp32 stream 189, bf16
-// 156 but 28 at 4096 x 2048), rows ahead by asynchronous copies to shared memory (173 /
-// 195), two pieces a thread in two CTAs (154 / 220).
+// (4.7 TB/s), 16384 x 6656, bf16 161 us (5.4), 16384 x 1024, fp32 44 us (5.3). Also tried:
+// rows ahead by asynchronous copies to shared memory (173 / 195), two pieces a thread in two
+// CTAs (154 / 220).
 #include "kernels.h"
 #include "norm.h"
 #include "rows.cuh"
 
 namespace lmoe {
 
-// Rows that a group takes at a time: all of their accesses are started before the first
-// is used and their sums share a barrier. Two of a bf16 stream (16384 x 6656 with one /
-// two / three: 217 / 182 / 203 us, three spill), one of an fp32 stream, whose rows are
-// twice as long (8192 x 6656: 163 / 161, 16384 x 1024: 44 / 48 us).
-constexpr int norm_rows(int s_size, int vpt) { return vpt > 1 ? 1 : s_size == 2 ? 2 : 1; }
+// How rows overlap. Narrow and fp32 streams: one piece (8 elements) a thread, about 32 warps
+// an SM, and of a bf16 stream two rows at a time (one barrier for both; 65536 x 256 28 us
+// either way). Wide bf16 streams: two pieces a thread, 16 warps an SM, and the next row on
+// its way in registers while this one is reduced: 16384 x 6656 182 -> 161 us, 4096 x 2048 20 ->
+// 17.8 (with the weight in registers too: 245 and 22 without). An fp32 stream's next row does not fit beside dw (8192 x 6656 163 -> 189 us), nor do two
+// rows of it (16384 x 1024 44 -> 48).
+constexpr int norm_rows(int s_size, int vpt) { return vpt > 1 || s_size > 2 ? 1 : 2; }
+constexpr bool norm_ahead(int vpt) { return vpt == 2; }
+
+// R rows of a group, groups rows apart, as they lie in memory: half the registers of their
+// fp32 values. A row past the last is zeros.
+template <typename YT, typename ST, bool DS, bool VEC, int VPT, int R>
+struct NormRows {
+  RowPiece<VEC, YT> dy[R][VPT];
+  RowPiece<VEC, ST> s[R][VPT], ds[R][VPT];
+  float rstd[R];
+  __device__ __forceinline__ void load(const NormBackwardArgs& a, long long t0, long long groups,
+                                       int warp, int warps, int lane) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long t = t0 + r * groups;
+      const int width = t < a.T ? a.d : 0;
+      rstd[r] = t < a.T ? a.rstd[t] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int chunk = j * warps + warp;
+        dy[r][j].load(static_cast<const YT*>(a.dy) + t * a.ld_dy, chunk, lane, width);
+        s[r][j].load(static_cast<const ST*>(a.s) + t * a.ld_s, chunk, lane, width);
+        if (DS)
+          ds[r][j].load(static_cast<const ST*>(a.d_sum) + t * a.ld_d_sum, chunk, lane, width);
+      }
+    }
+  }
+};
 
 template <typename YT, typename ST, bool DS, bool VEC, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rms_norm_backward_kernel(const NormBackwardArgs a) {
@@ -43,32 +71,34 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rms_norm_backward_kerne
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[j][k] = 0.0f;
-  // 8 elements of the weight: in L1 after the first row
-  auto weight = [&](int j, float* w) {
+  // 8 elements of the weight: in registers beside rows that are on their way, else in L1
+  // after the first row
+  auto load_weight = [&](int j, float* w) {
     if (a.weight_f32)
       row_load<VEC>(static_cast<const float*>(a.weight), j * warps + warp, lane, d, w);
     else
       row_load<VEC>(static_cast<const __nv_bfloat16*>(a.weight), j * warps + warp, lane, d, w);
   };
-  int turn = 0;
-  for (long long t0 = group; t0 < a.T; t0 += R * groups) {
-    // the rows as they lie in memory, half the registers of their fp32 values
-    RowPiece<VEC, YT> dy[R][VPT];
-    RowPiece<VEC, ST> s[R][VPT], ds[R][VPT];
-    float rstd[R];
+  float held[VPT][8];
+  if (norm_ahead(VPT)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long t = t0 + r * groups;
-      const int width = t < a.T ? d : 0;  // a row past the last is zeros
-      rstd[r] = t < a.T ? a.rstd[t] : 0.0f;
+    for (int j = 0; j < VPT; ++j) load_weight(j, held[j]);
+  }
+  auto weight = [&](int j, float* w) {
+    if (norm_ahead(VPT)) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int chunk = j * warps + warp;
-        dy[r][j].load(static_cast<const YT*>(a.dy) + t * a.ld_dy, chunk, lane, width);
-        s[r][j].load(static_cast<const ST*>(a.s) + t * a.ld_s, chunk, lane, width);
-        if (DS) ds[r][j].load(static_cast<const ST*>(a.d_sum) + t * a.ld_d_sum, chunk, lane, width);
-      }
+      for (int k = 0; k < 8; ++k) w[k] = held[j][k];
+    } else {
+      load_weight(j, w);
     }
+  };
+  int turn = 0;
+  NormRows<YT, ST, DS, VEC, VPT, R> next;
+  if (norm_ahead(VPT)) next.load(a, group, groups, warp, warps, lane);
+  for (long long t0 = group; t0 < a.T; t0 += R * groups) {
+    if (!norm_ahead(VPT)) next.load(a, t0, groups, warp, warps, lane);
+    const NormRows<YT, ST, DS, VEC, VPT, R> now = next;
+    if (norm_ahead(VPT)) next.load(a, t0 + groups, groups, warp, warps, lane);
     float dot[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) dot[r] = 0.0f;
@@ -79,12 +109,12 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rms_norm_backward_kerne
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float g[8], n[8];
-        dy[r][j].get(g);
-        s[r][j].get(n);
+        now.dy[r][j].get(g);
+        now.s[r][j].get(n);
         float part = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          n[k] *= rstd[r];
+          n[k] *= now.rstd[r];
           dw[j][k] = fmaf(g[k], n[k], dw[j][k]);
           part = fmaf(g[k] * w[k], n[k], part);
         }
@@ -114,18 +144,18 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rms_norm_backward_kerne
       for (int r = 0; r < R; ++r) {
         const long long t = t0 + r * groups;
         if (t >= a.T) break;
-        const float back = rstd[r] * (dot[r] / static_cast<float>(d));
+        const float back = now.rstd[r] * (dot[r] / static_cast<float>(d));
         float g[8], n[8], o[8];
-        dy[r][j].get(g);
-        s[r][j].get(n);
+        now.dy[r][j].get(g);
+        now.s[r][j].get(n);
         if constexpr (DS) {
-          ds[r][j].get(o);
+          now.ds[r][j].get(o);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[k] = 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] += rstd[r] * (g[k] * w[k] - n[k] * back);
+        for (int k = 0; k < 8; ++k) o[k] += now.rstd[r] * (g[k] * w[k] - n[k] * back);
         row_store<VEC>(static_cast<ST*>(a.dx) + t * a.ld_dx, chunk, lane, d, o);
         if (sizeof(ST) == 4 && a.dx16 != nullptr)
           row_store<VEC>(static_cast<__nv_bfloat16*>(a.dx16) + t * a.ld_dx16, chunk, lane, d, o);
@@ -190,14 +220,14 @@ struct Shape {
   int vpt, warps, rows, ctas;
 };
 
-Shape shape_of(long long T, int d, int sms) {
+Shape shape_of(long long T, int d, int sms, bool s_f32) {
   Shape p;
   const int chunks = (d + 255) / 256;
-  p.vpt = chunks <= 32 ? 1 : 4;
+  p.vpt = chunks > 32 ? 4 : !s_f32 && chunks > 4 ? 2 : 1;
   p.warps = (chunks + p.vpt - 1) / p.vpt;
   p.rows = p.warps == 1 ? 8 : 1;  // eight: what the kernel joins
-  // about 32 warps an SM: 24 / 32 / 40 take 22 / 20 / 22 us for 4096 x 2048 in bf16
-  int per_sm = 32 / (p.warps * p.rows);
+  // warps an SM: one piece a thread, 24 / 32 / 40: 22 / 20 / 22 us for 4096 x 2048 in bf16
+  int per_sm = (p.vpt == 2 ? 16 : 32) / (p.warps * p.rows);
   if (per_sm < 1) per_sm = 1;
   const long long want = (T + p.rows - 1) / p.rows, most = static_cast<long long>(per_sm) * sms;
   p.ctas = static_cast<int>(want < most ? want : most);
@@ -210,8 +240,11 @@ bool whole(const void* p, long long ld, int size, int unit) {
 
 template <typename YT, typename ST, bool DS, bool VEC>
 cudaError_t launch_vpt(const NormBackwardArgs& a, const Shape& p, cudaStream_t s) {
-  const auto kern = p.vpt == 1 ? rms_norm_backward_kernel<YT, ST, DS, VEC, 1>
-                               : rms_norm_backward_kernel<YT, ST, DS, VEC, 4>;
+  auto kern = rms_norm_backward_kernel<YT, ST, DS, VEC, 1>;
+  if (p.vpt == 4) kern = rms_norm_backward_kernel<YT, ST, DS, VEC, 4>;
+  if constexpr (sizeof(ST) == 2) {
+    if (p.vpt == 2) kern = rms_norm_backward_kernel<YT, ST, DS, VEC, 2>;
+  }
   return launch_kernel(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(32 * p.warps, p.rows), 0, s,
                        1, false, a);
 }
@@ -235,12 +268,13 @@ cudaError_t launch_sum(const NormBackwardArgs& a, const Shape& p, cudaStream_t s
 }  // namespace
 
 int norm_partials(long long T, int d, int sms) {
-  return shape_of(T, d, sms).ctas;
+  const int a = shape_of(T, d, sms, false).ctas, b = shape_of(T, d, sms, true).ctas;
+  return a > b ? a : b;
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, int sms, cudaStream_t s) {
   const PdlScope pdl(true);
-  const Shape p = shape_of(a.T, a.d, sms);
+  const Shape p = shape_of(a.T, a.d, sms, a.s_f32 != 0);
   cudaError_t e;
   if (a.dy_f32)
     e = a.s_f32 ? launch_sum<float, float>(a, p, s) : launch_sum<float, __nv_bfloat16>(a, p, s);
