@@ -725,16 +725,18 @@ def _device() -> int:
     return _raw_device()
 
 
-def _here(t, name: str) -> None:
-    # device pointers are the current device's: a tensor of another one is refused
-    if not (t.is_cuda and t.get_device() == _device()):
+# Checks of the block's operators. A small call is half Python, so the current device is
+# asked for once a call, and a message is put together only where it is raised.
+# get_device is -1 for a host tensor; device pointers are the current device's.
+def _not_here(t, name: str, dev: int) -> None:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
-def _token_rows(t, name: str, T: int, d: int, dtypes) -> int:
+def _token_rows(t, name: str, T: int, d: int, dtypes, dev: int) -> int:
     """Row stride of a [T, d] tensor whose rows are contiguous and do not overlap."""
-    _here(t, name)
-    if t.dtype not in dtypes or t.shape != (T, d):
+    if t.get_device() != dev or t.dtype not in dtypes or t.shape != (T, d):
+        _not_here(t, name, dev)
         raise ValueError(f"{name} must be [{T}, {d}] of type "
                          f"{' or '.join(str(x) for x in dtypes)}, got {list(t.shape)} {t.dtype}")
     step, inner = t.stride()
@@ -742,6 +744,16 @@ def _token_rows(t, name: str, T: int, d: int, dtypes) -> int:
     if (inner != 1 and d > 1) or ld < d:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return ld
+
+
+def _matrix(t, name: str, rows: int, cols: int, dtype, dev: int) -> int:
+    """Address of a contiguous [rows, cols]."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (rows, cols) or \
+            not t.is_contiguous():
+        _not_here(t, name, dev)
+        raise ValueError(f"{name} must be a contiguous {dtype} [{rows}, {cols}], got "
+                         f"{list(t.shape)} {t.dtype}")
+    return t.data_ptr()
 
 
 class GatedFFN:
@@ -752,7 +764,7 @@ class GatedFFN:
 
     def __init__(self, d: int, F: int, max_tokens: int = 1, training: bool = False):
         self.dims = latentmoe_ffn_dims(d, F, max_tokens, int(training))
-        self.device = None
+        self.d, self.F, self.device = d, F, None
         h = _c_void_p()
         check(load().latentmoe_ffn_create(ctypes.byref(self.dims), ctypes.byref(h)),
               "latentmoe_ffn_create")
@@ -774,20 +786,13 @@ class GatedFFN:
         if code != OK:
             raise LatentMoEError(code, what, load().latentmoe_ffn_last_cuda_error(self.handle))
 
-    def _matrix(self, t, name: str, rows: int, cols: int, dtype=None):
-        import torch
-        _here(t, name)
-        if not (t.shape == (rows, cols) and t.dtype is (dtype or torch.bfloat16) and
-                t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype or torch.bfloat16} "
-                             f"[{rows}, {cols}], got {list(t.shape)} {t.dtype}")
-        return t.data_ptr()
-
-    def _weights(self, w_g, w_u, w_d):
-        d, F = self.dims.hidden, self.dims.ffn
-        _need(_device() == self.device, "the handle belongs to another device than the current one")
-        return latentmoe_ffn_weights(self._matrix(w_g, "w_g", F, d), self._matrix(w_u, "w_u", F, d),
-                                     self._matrix(w_d, "w_d", d, F))
+    def _weights(self, w_g, w_u, w_d, b16, dev: int):
+        d, F = self.d, self.F
+        if dev != self.device:
+            raise ValueError("the handle belongs to another device than the current one")
+        return latentmoe_ffn_weights(_matrix(w_g, "w_g", F, d, b16, dev),
+                                     _matrix(w_u, "w_u", F, d, b16, dev),
+                                     _matrix(w_d, "w_d", d, F, b16, dev))
 
     def forward(self, x, w_g, w_u, w_d, save: bool = False, out=None, stream=None):
         """y [T, d] bf16 of x [T, d] bf16 (rows may be strided); with ``save`` (y, gate,
@@ -795,18 +800,24 @@ class GatedFFN:
         import torch
         if stream is not None:
             return _on_stream(stream, self.forward, x, w_g, w_u, w_d, save, out)
-        _need(x.dim() == 2, "x must be [T, d]")
-        T, d, F = x.shape[0], self.dims.hidden, self.dims.ffn
-        bf16 = (torch.bfloat16,)
-        ld_x = _token_rows(x, "x", T, d, bf16)
-        b16, dev = torch.bfloat16, x.device
-        y = torch.empty((T, d), dtype=b16, device=dev) if out is None else out
-        ld_y = d if out is None else _token_rows(y, "out", T, d, bf16)
-        gate = torch.empty((T, F), dtype=b16, device=dev) if save else None
-        up = torch.empty((T, F), dtype=b16, device=dev) if save else None
-        self._check(load().latentmoe_ffn_forward(
-            self.handle, ctypes.byref(self._weights(w_g, w_u, w_d)), x.data_ptr(), ld_x,
-            y.data_ptr(), ld_y, _ptr(gate), _ptr(up), T, _stream(None)), "latentmoe_ffn_forward")
+        if x.dim() != 2:
+            raise ValueError("x must be [T, d]")
+        T, d, F, b16, cur, dev = x.shape[0], self.d, self.F, torch.bfloat16, _device(), x.device
+        ld_x, ld_y = _token_rows(x, "x", T, d, (b16,), cur), d
+        w = self._weights(w_g, w_u, w_d, b16, cur)
+        if out is None:
+            y = torch.empty((T, d), dtype=b16, device=dev)
+        else:
+            y, ld_y = out, _token_rows(out, "out", T, d, (b16,), cur)
+        gate = up = at_gate = at_up = None
+        if save:
+            gate = torch.empty((T, F), dtype=b16, device=dev)
+            up = torch.empty((T, F), dtype=b16, device=dev)
+            at_gate, at_up = gate.data_ptr(), up.data_ptr()
+        code = load().latentmoe_ffn_forward(self.handle, ctypes.byref(w), x.data_ptr(), ld_x,
+                                            y.data_ptr(), ld_y, at_gate, at_up, T, _stream(None))
+        if code != OK:
+            self._check(code, "latentmoe_ffn_forward")
         return (y, gate, up) if save else y
 
     def backward(self, dy, x, gate, up, w_g, w_u, w_d, dw_dtype=None, out=None,
@@ -819,42 +830,40 @@ class GatedFFN:
         if stream is not None:
             return _on_stream(stream, self.backward, dy, x, gate, up, w_g, w_u, w_d, dw_dtype, out,
                               accumulate, need)
-        _need(dy.dim() == 2, "dy must be [T, d]")
-        T, d, F = dy.shape[0], self.dims.hidden, self.dims.ffn
-        bf16 = (torch.bfloat16,)
-        out = dict(out or {})
-        names = [n for n in ("dx", "dw_g", "dw_u", "dw_d") if n in need]
-        given = [out[n].dtype for n in names if n != "dx" and n in out]
-        dt = dw_dtype or (given[0] if given else torch.bfloat16)
-        _need(not accumulate or all(n in out for n in names if n != "dx"),
-              "accumulate needs the weights' gradients in out")
-        g = latentmoe_ffn_grad(dy=dy.data_ptr(), ld_dy=_token_rows(dy, "dy", T, d, bf16),
-                               x=x.data_ptr(), ld_x=_token_rows(x, "x", T, d, bf16),
-                               gate=self._matrix(gate, "gate", T, F),
-                               up=self._matrix(up, "up", T, F), accumulate=int(accumulate))
-        got = {}
-        for n in names:
-            if n == "dx":
-                if n in out:
-                    t = out[n]
-                    g.ld_dx = _token_rows(t, n, T, d, bf16)
-                else:
-                    t = torch.empty((T, d), dtype=torch.bfloat16, device=dy.device)
-                g.dx = t.data_ptr()
+        if dy.dim() != 2:
+            raise ValueError("dy must be [T, d]")
+        T, d, F, b16, cur, dev = dy.shape[0], self.d, self.F, torch.bfloat16, _device(), dy.device
+        ld_dy, ld_x = _token_rows(dy, "dy", T, d, (b16,), cur), _token_rows(x, "x", T, d, (b16,), cur)
+        w = self._weights(w_g, w_u, w_d, b16, cur)
+        out = out or {}
+        dt = dw_dtype or next((out[n].dtype for n in ("dw_g", "dw_u", "dw_d")
+                               if n in need and n in out), b16)
+        got, at, ld_dx = {}, [None] * 4, 0
+        for i, (n, rows, cols) in enumerate((("dx", T, d), ("dw_g", F, d), ("dw_u", F, d),
+                                             ("dw_d", d, F))):
+            if n not in need:
+                continue
+            if n not in out:
+                if accumulate and i:
+                    raise ValueError("accumulate needs the weights' gradients in out")
+                t = torch.empty((rows, cols), dtype=dt if i else b16, device=dev)
+                at[i] = t.data_ptr()
+            elif i:
+                t = out[n]
+                at[i] = _matrix(t, n, rows, cols, dt, cur)
             else:
-                shape = (d, F) if n == "dw_d" else (F, d)
-                if n in out:
-                    t = out[n]
-                    at = self._matrix(t, n, shape[0], shape[1], dt)
-                else:
-                    t = torch.empty(shape, dtype=dt, device=dy.device)
-                    at = t.data_ptr()
-                g.dw_dtype = _dtype_code(t, n)
-                setattr(g, n, at)
+                t = out[n]
+                at[i], ld_dx = t.data_ptr(), _token_rows(t, n, T, d, (b16,), cur)
             got[n] = t
-        self._check(load().latentmoe_ffn_backward(
-            self.handle, ctypes.byref(self._weights(w_g, w_u, w_d)), ctypes.byref(g), T,
-            _stream(None)), "latentmoe_ffn_backward")
+        if dt is not b16 and dt is not torch.float32:
+            raise ValueError("the weights' gradients must be bfloat16 or float32")
+        g = latentmoe_ffn_grad(dy.data_ptr(), x.data_ptr(), _matrix(gate, "gate", T, F, b16, cur),
+                               _matrix(up, "up", T, F, b16, cur), at[0], at[1], at[2], at[3], ld_dy,
+                               ld_x, ld_dx, BF16 if dt is b16 else FP32, 1 if accumulate else 0)
+        code = load().latentmoe_ffn_backward(self.handle, ctypes.byref(w), ctypes.byref(g), T,
+                                             _stream(None))
+        if code != OK:
+            self._check(code, "latentmoe_ffn_backward")
         return got
 
     def set_sm_pairs(self, mode: int) -> None:
@@ -875,9 +884,9 @@ class GatedFFN:
         return v.value
 
 
-def _norm_weight(weight, d: int) -> int:
-    _here(weight, "weight")
-    if weight.shape != (d,) or not weight.is_contiguous():
+def _norm_weight(weight, d: int, dev: int) -> int:
+    if weight.get_device() != dev or weight.shape != (d,) or not weight.is_contiguous():
+        _not_here(weight, "weight", dev)
         raise ValueError(f"weight must be a contiguous [{d}]")
     return _dtype_code(weight, "weight")
 
@@ -902,21 +911,22 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, quantize: Optional[str
     if quantize not in (None, "token", "block"):
         raise ValueError('quantize must be None, "token" or "block"')
     # torch.empty, not new_empty: half the time of a call that takes 3 us
-    f32, empty, dev, dt = torch.float32, torch.empty, x.device, x.dtype
+    f32, empty, dev, dt, cur = torch.float32, torch.empty, x.device, x.dtype, _device()
     both = (torch.bfloat16, f32)
     T, d = x.shape
-    ld_x, w_code = _token_rows(x, "x", T, d, both), _norm_weight(weight, d)
+    ld_x, w_code = _token_rows(x, "x", T, d, both, cur), _norm_weight(weight, d, cur)
     rstd = empty(T, dtype=f32, device=dev)
     out = {"rstd": rstd}
     r = s = y = codes = scales = None
     ld_r = ld_s = r_code = y_code = block = 0
     if residual is not None:
-        r, ld_r, r_dt = residual.data_ptr(), _token_rows(residual, "residual", T, d, both), residual.dtype
+        ld_r, r_dt = _token_rows(residual, "residual", T, d, both, cur), residual.dtype
+        r = residual.data_ptr()
         r_code = FP32 if r_dt is f32 else BF16
         if out_sum is None:
             s_out, ld_s = empty((T, d), dtype=r_dt, device=dev), d
         else:
-            s_out, ld_s = out_sum, _token_rows(out_sum, "out_sum", T, d, (r_dt,))
+            s_out, ld_s = out_sum, _token_rows(out_sum, "out_sum", T, d, (r_dt,), cur)
         out["sum"] = s_out
         s = s_out.data_ptr()
     elif out_sum is not None:
@@ -951,15 +961,16 @@ def rms_norm_backward(dy, s, weight, rstd, d_sum=None, dw: bool = True, dx_bf16:
         return _on_stream(stream, rms_norm_backward, dy, s, weight, rstd, d_sum, dw, dx_bf16)
     if dy.dim() != 2:
         raise ValueError("dy must be [T, d]")
-    f32, empty, dev = torch.float32, torch.empty, dy.device
+    f32, empty, dev, cur = torch.float32, torch.empty, dy.device, _device()
     both = (torch.bfloat16, f32)
     T, d = dy.shape
-    _here(rstd, "rstd")
-    if rstd.dtype is not f32 or rstd.shape != (T,) or not rstd.is_contiguous():
+    if rstd.get_device() != cur or rstd.dtype is not f32 or rstd.shape != (T,) or \
+            not rstd.is_contiguous():
+        _not_here(rstd, "rstd", cur)
         raise ValueError(f"rstd must be a contiguous float32 [{T}]")
-    ld_dy, ld_s = _token_rows(dy, "dy", T, d, both), _token_rows(s, "s", T, d, both)
-    w_code = _norm_weight(weight, d)
-    ld_ds = 0 if d_sum is None else _token_rows(d_sum, "d_sum", T, d, (s.dtype,))
+    ld_dy, ld_s = _token_rows(dy, "dy", T, d, both, cur), _token_rows(s, "s", T, d, both, cur)
+    w_code = _norm_weight(weight, d, cur)
+    ld_ds = 0 if d_sum is None else _token_rows(d_sum, "d_sum", T, d, (s.dtype,), cur)
     dx = empty((T, d), dtype=s.dtype, device=dev)
     out = {"dx": dx}
     dx16 = ws = grad = None
