@@ -619,9 +619,8 @@ int latentmoe_muon_destroy(latentmoe_muon_t h);
  *
  * bf16 operands and fp32 accumulators; the activation in fp32, from the
  * accumulators (forward) or from the stored bf16 gate and up (backward). h, dg and
- * du are rounded to bf16 between the products. No atomics: results are bitwise
- * reproducible. Rows of x and dy past T are not read, rows of y and dx past T not
- * written. */
+ * du are rounded to bf16 between the products. Results are bitwise reproducible.
+ * Rows of x and dy past T are not read, rows of y and dx past T not written. */
 typedef struct latentmoe_ffn* latentmoe_ffn_t;
 
 /* hidden d and ffn F: multiples of 8 up to 65536. max_tokens (up to 2^22) bounds T

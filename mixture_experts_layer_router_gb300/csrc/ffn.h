@@ -50,9 +50,9 @@ cudaError_t launch_ffn(int epi, int shape, const FfnArgs& a, int sms, cudaStream
 
 // Operands of fewer than kFfnLeastRows rows, padded: a TMA load of a box of a matrix
 // with fewer than 8 rows (the height of a swizzle pattern) takes several times as long
-// as of one with 8, most of them outside alike. 8704 x 10240 on tiles, 4 tokens: backward
-// 545 us, with padding 319; 8 tokens 319. xs, dys [8, d] = x and dy [tokens, d] (x null: none),
-// rows of h, dg and du from `tokens` to 8: zeros.
+// as of one with 8, most of them outside alike. 8704 x 10240 forward on single tiles, 4
+// tokens 407 us, seen as 8 rows 159; 8 tokens 158. xs, dys [8, d] = x and dy [tokens, d]
+// (x null: none), rows of h, dg and du from `tokens` to 8: zeros.
 constexpr int kFfnLeastRows = 8;
 cudaError_t launch_ffn_pad(const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* dy,
                            long long ld_dy, int tokens, int d, int F, __nv_bfloat16* xs,
