@@ -241,6 +241,30 @@ def test_stream_and_graph():
     assert m.status() == 0
 
 
+def test_two_handles_at_once():
+    """Handles share nothing: calls of every kernel on two streams at the same time."""
+    gh.lib()
+    d, F = 264, 520
+    sets = []
+    for i, T in enumerate((5, 16, 100, 700)):
+        x, w = block(T, d, F, seed=10 * i)
+        dy, gate, up = rand((T, d), i + 1, 1e-2), rand((T, F), i + 2), rand((T, F), i + 3)
+        two = [capi.GatedFFN(d, F, max_tokens=T, training=True) for _ in range(2)]
+        want = (two[0].forward(x, **w), two[0].backward(dy, x, gate, up, **w))
+        sets.append((x, w, dy, gate, up, two, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for x, w, dy, gate, up, two, want in sets:
+            for m, st in zip(two, streams):
+                got.append((m.forward(x, **w, stream=st), m.backward(dy, x, gate, up, **w, stream=st), want))
+    torch.cuda.synchronize()
+    for y, g, want in got:
+        assert torch.equal(y, want[0]) and all(torch.equal(g[n], want[1][n]) for n in g)
+    assert all(m.status() == 0 for s in sets for m in s[5])
+
+
 def test_against_differences():
     """sum(dy y) in float64 along the gradient's own direction, for x and each weight:
     central differences are exact to 1e-6 here (h 1e-4); the gradient's own roundings
